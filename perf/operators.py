@@ -293,7 +293,7 @@ def _plain_plan(c, s):
     n = torch.where(bad | gone, 0, new)
     end = torch.cumsum(n, 0)
     full = ~bad & (kv + n > width * B)
-    many = ~bad & ~full & (end > N)
+    many = ~bad & ~full & (n > 0) & (end > N)
     held = (kv + B - 1) // B
     need = torch.where(bad | gone | full | many, 0, (kv + n + B - 1) // B - held)
     back = torch.where(gone, held, 0)
