@@ -1,0 +1,341 @@
+// kvc_attn_simt.cu -- attention of a chunk of new tokens over a paged cache in
+// FP32 arithmetic.
+//
+// One pass over the keys with the running maximum and sum of the softmax: with
+// x_j = scale log2(e) q.k_j, a row keeps m = max x_j, l = sum exp2(x_j - m) and
+// O = sum exp2(x_j - m) v_j, and scales l and O by exp2(m_old - m_new) when a
+// tile raises m.  out = O / l and lse = ln(2) (m + log2 l); a row that sees no
+// key keeps m = -inf, l = 0 and gives out = 0, lse = -inf.
+//
+// A tile is 64 keys.  The rows of an item are (token, query head of the KV
+// head's group), so that K and V are read once for the whole group.
+#include <cuda_bf16.h>
+
+#include "kvc_attn_sched.cuh"
+#include "kvc_paged_internal.h"
+
+namespace kvc {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;
+constexpr int kSlotRows = 64;
+constexpr int kMaxCtas = 320;
+
+__device__ __forceinline__ float4 load4(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+struct Smem {
+  Shared sched;
+  int32_t last;
+};
+
+// T: element type.  RPT: rows per thread; an item has 16 * RPT rows.  DC:
+// 64-column groups of d per thread.
+template <typename T, int RPT, int DC>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, const SchedArgs sa) {
+  extern __shared__ float4 smem4[];
+  __shared__ Smem sh;
+  constexpr int kRows = 16 * RPT;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int d = a.d, dp = d + 4, dv = d >> 2;
+  float* Qs = reinterpret_cast<float*>(smem4);      // [kRows][dp]
+  float* Ks = Qs + kRows * dp;                      // [kTile][dp]
+  float* Vs = Ks + kTile * dp;                      // [kTile][d]
+  float* Ps = Vs + kTile * d;                       // [kRows][kTile + 4]
+  constexpr int kPp = kTile + 4;
+
+  Walker w = walker_begin<kThreads>(sa, &sh.sched, a.dev_status);
+  int32_t* counters = static_cast<int32_t*>(a.workspace);
+  float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
+  const size_t slot_n = slot_floats(kSlotRows, d);
+  const T* poolK = static_cast<const T*>(a.pool[0].base) + a.layer * a.pool[0].s_layer;
+  const T* poolV = static_cast<const T*>(a.pool[1].base) + a.layer * a.pool[1].s_layer;
+
+  Item it;
+  while (w.next(sa, &it)) {
+    const int rows = it.nt * a.G;
+    // the item's query rows; rows past the item are zero
+    for (int i = tid; i < kRows * dv; i += kThreads) {
+      const int row = i / dv, c = (i - row * dv) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < rows) {
+        const int tok = row / a.G, g = row - tok * a.G;
+        v = load4(static_cast<const T*>(a.q) + (it.q0 + tok) * a.q_tok +
+                  (it.h * a.G + g) * a.q_head + c);
+      }
+      *reinterpret_cast<float4*>(Qs + row * dp + c) = v;
+    }
+    float m[RPT], l[RPT];
+    int key_lo[RPT], key_hi[RPT];              // keys in sight of the thread's rows
+    float4 o[RPT][DC];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = ty * RPT + i;
+      const int pos = it.pos0 + row / a.G;
+      key_hi[i] = row < rows ? (a.causal ? min(it.kv, pos + 1) : it.kv) : 0;
+      key_lo[i] = a.window > 0 ? pos - a.window + 1 : 0;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+
+    for (int t = 0; t < it.ntiles; ++t) {
+      const int k0 = (it.tile0 + t) * kTile;
+      __syncthreads();                          // the previous tile has been read
+      for (int i = tid; i < kTile * dv; i += kThreads) {
+        const int n = i / dv, c = (i - n * dv) * 4;
+        const int tok = k0 + n;
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        if (tok < it.kv) {
+          const int blk = tok / a.B;
+          const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
+          if (page >= 0 && page < a.P) {
+            const int64_t off = tok - blk * a.B;
+            k = load4(poolK + page * a.pool[0].s_req + it.h * a.pool[0].s_head +
+                      off * a.pool[0].s_tok + c);
+            v = load4(poolV + page * a.pool[1].s_req + it.h * a.pool[1].s_head +
+                      off * a.pool[1].s_tok + c);
+          } else {
+            atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
+          }
+        }
+        *reinterpret_cast<float4*>(Ks + n * dp + c) = k;
+        *reinterpret_cast<float4*>(Vs + n * d + c) = v;
+      }
+      __syncthreads();
+
+      float s[RPT][4];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      for (int c = 0; c < d; c += 4) {
+        float4 kq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          kq[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * dp + c);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * RPT + i) * dp + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(q.x, kq[j].x, s[i][j]);
+            s[i][j] = fmaf(q.y, kq[j].y, s[i][j]);
+            s[i][j] = fmaf(q.z, kq[j].z, s[i][j]);
+            s[i][j] = fmaf(q.w, kq[j].w, s[i][j]);
+          }
+        }
+      }
+      bool whole = true;                        // every row of the thread sees the whole tile
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tok = k0 + tx + 16 * j;
+          const bool see = tok >= key_lo[i] && tok < key_hi[i];
+          s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+        whole = whole && (ty * RPT + i >= rows || (k0 >= key_lo[i] && k0 + kTile <= key_hi[i]));
+#pragma unroll
+        for (int b = 8; b > 0; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
+        const float m_new = fmaxf(m[i], mx);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float f = exp2f(m[i] - ref);      // 0 while nothing was seen
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(s[i][j] - ref);
+          sum += p;
+          Ps[(ty * RPT + i) * kPp + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int b = 8; b > 0; b >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
+        l[i] = l[i] * f + sum;
+        m[i] = m_new;
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          o[i][c].x *= f;
+          o[i][c].y *= f;
+          o[i][c].z *= f;
+          o[i][c].w *= f;
+        }
+      }
+      __syncwarp();                             // a warp reads the P rows it wrote
+      for (int n = 0; n < kTile; ++n) {
+        float p[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) p[i] = Ps[(ty * RPT + i) * kPp + n];
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const int col = tx * 4 + c * 64;
+          if (col < d) {
+            const float4 v = *reinterpret_cast<const float4*>(Vs + n * d + col);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+              // a key out of a row's sight adds nothing, whatever its value row holds
+              if (!whole && !(k0 + n >= key_lo[i] && k0 + n < key_hi[i])) continue;
+              o[i][c].x = fmaf(p[i], v.x, o[i][c].x);
+              o[i][c].y = fmaf(p[i], v.y, o[i][c].y);
+              o[i][c].z = fmaf(p[i], v.z, o[i][c].z);
+              o[i][c].w = fmaf(p[i], v.w, o[i][c].w);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+    if (it.nparts == 1) {
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int row = ty * RPT + i;
+        if (row >= rows) continue;
+        const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const int col = tx * 4 + c * 64;
+          if (col < d)
+            store4(static_cast<T*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
+                   make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv,
+                               o[i][c].w * inv));
+        }
+        if (a.lse != nullptr && tx == 0)
+          a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] =
+              l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+      }
+      continue;
+    }
+
+    // a divided item: leave the partial rows, and join them if all others have
+    float* slot = slots + (static_cast<size_t>(blockIdx.x) * 2 + slot_of(it.part)) * slot_n;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = ty * RPT + i;
+      if (row >= rows) continue;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const int col = tx * 4 + c * 64;
+        if (col < d) store4(slot + row * d + col, o[i][c]);
+      }
+      if (tx == 0) {
+        slot[kSlotRows * d + row] = m[i];
+        slot[kSlotRows * d + kSlotRows + row] = l[i];
+      }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) sh.last = atomicAdd(counters + it.cta0, 1) == it.nparts - 1;
+    __syncthreads();
+    if (!sh.last) continue;
+    __threadfence();
+    if (tid == 0) counters[it.cta0] = 0;
+    for (int i = tid; i < rows * dv; i += kThreads) {
+      const int row = i / dv, col = (i - row * dv) * 4;
+      float M = -INFINITY;
+      for (int p = 0; p < it.nparts; ++p) {
+        const float* ps = slots + (static_cast<size_t>(it.cta0 + p) * 2 + slot_of(p)) * slot_n;
+        M = fmaxf(M, __ldcg(ps + kSlotRows * d + row));
+      }
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < it.nparts; ++p) {
+        const float* ps = slots + (static_cast<size_t>(it.cta0 + p) * 2 + slot_of(p)) * slot_n;
+        const float pm = __ldcg(ps + kSlotRows * d + row);
+        const float pl = __ldcg(ps + kSlotRows * d + kSlotRows + row);
+        if (pl == 0.f) continue;
+        const float f = part_weight(pm, pl, M);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + row * d + col));
+        L = fmaf(pl, f, L);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
+      store4(static_cast<T*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
+             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (a.lse != nullptr && col == 0)
+        a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+}
+
+template <typename T, int RPT, int DC>
+cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const int rows = 16 * RPT;
+  const size_t smem = sizeof(float) * (static_cast<size_t>(rows) * (a.d + 4) + kTile * (a.d + 4) +
+                                       kTile * a.d + rows * (kTile + 4));
+  auto* fn = attn_simt_kernel<T, RPT, DC>;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  SchedArgs s{};
+  s.q_start = a.q_start;
+  s.kv_lens = a.kv_lens;
+  s.R = a.R;
+  s.H = a.H;
+  s.N = a.N;
+  s.kv_cap = a.width * a.B;
+  s.causal = a.causal;
+  s.window = a.window;
+  s.tok_item = rows / a.G;
+  s.group_tok = kTile;
+  s.group_tiles = 1;
+  s.tile_tok = kTile;
+  const int per_sm = smem * 2 + 4096 <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
+  const int grid = di.sm_count * per_sm < kMaxCtas ? di.sm_count * per_sm : kMaxCtas;
+  fn<<<grid, kThreads, smem, stream>>>(a, s);
+  return cudaGetLastError();
+}
+
+template <typename T, int RPT>
+cudaError_t launch_d(const AttnArgs& a, cudaStream_t stream) {
+  switch ((a.d + 63) / 64) {
+    case 1: return launch_one<T, RPT, 1>(a, stream);
+    case 2: return launch_one<T, RPT, 2>(a, stream);
+    case 3: return launch_one<T, RPT, 3>(a, stream);
+    default: return launch_one<T, RPT, 4>(a, stream);
+  }
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(kvc_dtype, int d, int) {
+  return kAttnCounterBytes + kMaxCtas * 2 * slot_floats(kSlotRows, d) * sizeof(float);
+}
+
+cudaError_t launch_attn_simt(const AttnArgs& a, kvc_dtype dtype, cudaStream_t stream) {
+  if (dtype == KVC_BF16) return launch_d<__nv_bfloat16, 4>(a, stream);
+  return launch_d<float, 4>(a, stream);
+}
+
+}  // namespace kvc

@@ -1,0 +1,61 @@
+// kvc_paged_internal.h -- launch interface between the host layer of the paged
+// cache (kvc_paged.cu) and its kernels.  Not part of the public ABI.
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// Requests of one kvc_page_plan call: their scans live in shared memory.
+constexpr int kMaxPlanRequests = 4096;
+
+struct PlanArgs {
+  const int32_t* new_lens;
+  const int32_t* kv_in;
+  int32_t* kv_out;
+  int32_t* table;
+  int32_t* free_pages;
+  const int32_t* n_free_in;
+  int32_t* n_free_out;
+  int32_t* q_start;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* status;
+  int32_t R, P, B, width, max_tokens;
+};
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct WriteArgs {
+  View src[2], pool[2];       // src [Rs, nl, H, T, d]; pool [P, L, H, B, d]
+  const int64_t* slots;       // [Rs * T]
+  int64_t rows;               // Rs * T
+  int64_t n_slots;            // P * B
+  int32_t T, B, L0, nl, H;
+  int32_t vec_row;            // 16-byte vectors per row
+  int32_t elem;               // bytes per element
+};
+cudaError_t launch_page_write(const WriteArgs& a, cudaStream_t stream);
+
+// Paged attention.  q and out are [N, Hq, d] with element strides.
+struct AttnArgs {
+  const void* q;
+  void* out;
+  float* lse;                 // [N, Hq] or nullptr
+  int64_t q_tok, q_head, o_tok, o_head;
+  View pool[2];               // [P, L, H, B, d]
+  const int32_t* table;       // [R, width]
+  const int32_t* q_start;     // [R + 1]
+  const int32_t* kv_lens;     // [R]
+  int32_t R, N, H, G, d, P, L, B, width, layer, causal, window;
+  float scale_log2;           // scale * log2(e)
+  void* workspace;
+  int32_t* dev_status;
+};
+
+// Bytes of the workspace: arrival counters (zero between calls), then the
+// partial rows of divided items.
+constexpr size_t kAttnCounterBytes = 8192;
+size_t attn_workspace_bytes(kvc_dtype dtype, int d, int G);
+cudaError_t launch_attn_simt(const AttnArgs& a, kvc_dtype dtype, cudaStream_t stream);
+
+}  // namespace kvc

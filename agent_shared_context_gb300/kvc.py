@@ -45,9 +45,17 @@ EXPORTS = ("kvc_version", "kvc_status_string", "kvc_last_error",
            "kvc_build_states_workspace", "kvc_build_states", "kvc_match_anchors",
            "kvc_apply_correction", "kvc_chain_edge_workspace", "kvc_chain_edge",
            "kvc_selftest_bounded_wait", "kvc_chain_edge_noalloc", "kvc_pool_insert",
-           "kvc_build_representation", "kvc_match_representation")
+           "kvc_build_representation", "kvc_match_representation",
+           "kvc_page_plan", "kvc_page_write", "kvc_paged_attention_workspace",
+           "kvc_paged_attention")
 
 KVC_NOALLOC_MAX_UNITS = 262144
+
+KVC_PLAN_OK = 0
+KVC_PLAN_NO_PAGES = 1
+KVC_PLAN_ROW_FULL = 2
+KVC_PLAN_INVALID = 3
+KVC_PLAN_TOKENS = 4
 
 
 class KvcError(RuntimeError):
@@ -83,7 +91,23 @@ class kvc_params(ctypes.Structure):
                 ("omega_c", ctypes.c_void_p)]
 
 
+class kvc_paged(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("L", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("d", ctypes.c_int32), ("R", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class kvc_attn_params(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("layer", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_s_tok", ctypes.c_int64),
+                ("q_s_head", ctypes.c_int64), ("out_s_tok", ctypes.c_int64),
+                ("out_s_head", ctypes.c_int64)]
+
+
 _VIEW = kvc_cache_view
+_PG_P = ctypes.POINTER(kvc_paged)
+_ATT_P = ctypes.POINTER(kvc_attn_params)
 _SEG_P = ctypes.POINTER(kvc_segments)
 _PRM_P = ctypes.POINTER(kvc_params)
 _VP = ctypes.c_void_p
@@ -122,6 +146,18 @@ lib.kvc_match_representation.restype = _ST
 lib.kvc_match_representation.argtypes = [_SEG_P, _PRM_P, _VP, _VP, _VP, _VP, _VP, _VP]
 lib.kvc_selftest_bounded_wait.restype = _ST
 lib.kvc_selftest_bounded_wait.argtypes = [ctypes.c_int32, _VP, _VP]
+
+lib.kvc_page_plan.restype = _ST
+lib.kvc_page_plan.argtypes = [_PG_P, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP,
+                              _VP, _VP]
+lib.kvc_page_write.restype = _ST
+lib.kvc_page_write.argtypes = [_PG_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                               _VIEW, _VIEW, _VP, _VIEW, _VIEW, _VP]
+lib.kvc_paged_attention_workspace.restype = ctypes.c_size_t
+lib.kvc_paged_attention_workspace.argtypes = [_PG_P, _ATT_P]
+lib.kvc_paged_attention.restype = _ST
+lib.kvc_paged_attention.argtypes = [_PG_P, _ATT_P, _VP, _VIEW, _VIEW, _VP, _VP, _VP, _VP, _VP, _VP,
+                                    ctypes.c_size_t, _VP, _VP]
 
 
 # ------------------------------------------------------------------- helpers
@@ -354,3 +390,70 @@ def _v(x) -> kvc_cache_view:
     if isinstance(x, kvc_cache_view):
         return x
     return cache_view(x)
+
+
+# ---------------------------------------------------------------- paged caches
+def paged(n_pages: int, page_size: int, L: int, H: int, d: int, dtype: str, R: int,
+          max_blocks: int) -> kvc_paged:
+    """Descriptor of page pools [n_pages, L, H, page_size, d] and of block
+    tables [R, max_blocks]; ``dtype`` is "bf16" or "f32"."""
+    return kvc_paged(n_pages, page_size, L, H, d, R, max_blocks,
+                     KVC_BF16 if dtype in ("bf16", KVC_BF16) else
+                     (KVC_F32 if dtype in ("f32", KVC_F32) else int(dtype)))
+
+
+def attn_params(q, out, layer: int = 0, scale: float = 0.0, causal: bool = True,
+                window: int = 0) -> kvc_attn_params:
+    """Attention parameters for query and output tensors [N, Hq, d] (any token
+    and head strides, d contiguous); ``scale`` 0 means 1 / sqrt(d)."""
+    for t in (q, out):
+        if t.dim() != 3 or (t.stride(-1) != 1 and t.shape[-1] > 1) or t.shape != q.shape:
+            raise ValueError("q and out are [N, Hq, d] with a contiguous last dimension")
+    N, Hq, d = q.shape
+    return kvc_attn_params(Hq, N, layer, int(causal), window, scale if scale else d ** -0.5,
+                           q.stride(0), q.stride(1), out.stride(0), out.stride(1))
+
+
+def kvc_page_plan(pg: kvc_paged, new_lens: Ptr, kv_lens: Ptr, kv_lens_out: Ptr, block_table: Ptr,
+                  free_pages: Ptr, n_free: Ptr, n_free_out: Ptr, q_start: Ptr, slot_map: Ptr,
+                  positions: Ptr, plan_status: Ptr, stream=None,
+                  max_tokens: Optional[int] = None, check: bool = True) -> int:
+    """Block tables, slots and positions of a step's new tokens.
+    ``max_tokens`` is the length of ``slot_map`` and ``positions`` (taken from
+    the tensor if not given)."""
+    if max_tokens is None:
+        max_tokens = slot_map.numel()
+    st = lib.kvc_page_plan(ctypes.byref(pg), _addr(new_lens), _addr(kv_lens), _addr(kv_lens_out),
+                           _addr(block_table), _addr(free_pages), _addr(n_free), _addr(n_free_out),
+                           max_tokens, _addr(q_start), _addr(slot_map), _addr(positions),
+                           _addr(plan_status), _stream(stream))
+    return _done(st, "kvc_page_plan", check)
+
+
+def kvc_page_write(pg: kvc_paged, src_K, src_V, slot_map: Ptr, pool_K, pool_V, layer: int = 0,
+                   stream=None, shape: Optional[Sequence[int]] = None, check: bool = True) -> int:
+    """Rows of ``src_K`` / ``src_V`` [n_src, n_layers, H, T, d] into the slots
+    ``slot_map`` [n_src, T] of layers ``layer`` .. of the pools.  Raw views
+    need ``shape`` = (n_src, n_layers, T)."""
+    n, nl, T = shape if shape is not None else (src_K.shape[0], src_K.shape[1], src_K.shape[3])
+    st = lib.kvc_page_write(ctypes.byref(pg), n, T, layer, nl, _v(src_K), _v(src_V),
+                            _addr(slot_map), _v(pool_K), _v(pool_V), _stream(stream))
+    return _done(st, "kvc_page_write", check)
+
+
+def kvc_paged_attention_workspace(pg: kvc_paged, at: kvc_attn_params) -> int:
+    return int(lib.kvc_paged_attention_workspace(ctypes.byref(pg), ctypes.byref(at)))
+
+
+def kvc_paged_attention(pg: kvc_paged, at: kvc_attn_params, q: Ptr, pool_K, pool_V,
+                        block_table: Ptr, q_start: Ptr, kv_lens: Ptr, out: Ptr, workspace: Ptr,
+                        dev_status: Ptr, lse: Ptr = None, stream=None,
+                        workspace_bytes: Optional[int] = None, check: bool = True) -> int:
+    """Attention of every request's new tokens over its pages.  The first
+    8,192 bytes of ``workspace`` must be zero before its first use."""
+    ws_bytes = _nbytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    st = lib.kvc_paged_attention(ctypes.byref(pg), ctypes.byref(at), _addr(q), _v(pool_K),
+                                 _v(pool_V), _addr(block_table), _addr(q_start), _addr(kv_lens),
+                                 _addr(out), _addr(lse), _addr(workspace), ws_bytes,
+                                 _addr(dev_status), _stream(stream))
+    return _done(st, "kvc_paged_attention", check)

@@ -101,7 +101,7 @@ extern "C" {
 #endif
 
 #define KVC_VERSION_MAJOR 0
-#define KVC_VERSION_MINOR 3
+#define KVC_VERSION_MINOR 4
 
 typedef enum kvc_status {
   KVC_OK = 0,
@@ -396,6 +396,144 @@ kvc_status kvc_chain_edge_noalloc(int32_t edge, const kvc_segments* seg, const k
  * ------------------------------------------------------------------------- */
 kvc_status kvc_selftest_bounded_wait(int32_t max_polls, int32_t* dev_status,
                                      cudaStream_t stream);
+
+/* ===========================================================================
+ * Paged caches: serving from the corrected caches.
+ *
+ * A corrected cache is attended over by its agent's new tokens.  The calls
+ * below keep caches in pages: pool_K and pool_V are cache views
+ * [P, L, H, B, d] (P pages of B token rows; s_req is the page stride), so any
+ * physical order that a kvc_cache_view can express is a pool, and a dense
+ * cache [R, L, H, T, d] is a pool of R pages of T rows.  The pages hold the
+ * keys and values of the tokens that the chain corrected (listing, Figure
+ * 1(c)) followed by the agent's own (PF) tokens; the listing's serving system
+ * keeps its caches in a serving engine that the pages do not describe.
+ *
+ * Layouts and conventions (besides those above)
+ * ---------------------------------------------
+ * block_table  [R, max_blocks] int32: page of tokens [b B, (b + 1) B) of a
+ *              request; entries at or beyond ceil(kv_len / B) mean nothing.
+ * kv_lens      [R] int32: tokens of a request in the cache.
+ * q_start      [R + 1] int32: the new tokens of request r are rows
+ *              [q_start[r], q_start[r + 1]) of the packed token arrays.
+ * slot_map     int64: slot = page * B + row of a token, -1 for none.
+ * The lengths and tables are DEVICE memory and are read by the kernels: no
+ * call waits for the device, and a captured CUDA graph replays with new ones.
+ * Whatever they hold, no kernel reads or writes outside the buffers of the
+ * descriptors.
+ * ======================================================================== */
+typedef struct kvc_paged {
+  int32_t n_pages;      /* P, 1 .. 2^30                                      */
+  int32_t page_size;    /* B >= 1 token rows per page, any number            */
+  int32_t L;            /* layers of the pool                                */
+  int32_t H;            /* KV heads                                          */
+  int32_t d;            /* head dim: bf16 {64, 128}; f32 4..256, d % 4 == 0   */
+  int32_t R;            /* requests (rows of the block table), >= 0          */
+  int32_t max_blocks;   /* columns of the block table; max_blocks * B <= 2^30 */
+  kvc_dtype dtype;      /* of pools, queries and outputs                     */
+} kvc_paged;
+
+/* Status of one request in kvc_page_plan. */
+typedef enum kvc_plan_status {
+  KVC_PLAN_OK = 0,
+  KVC_PLAN_NO_PAGES = 1,   /* the free pages ran out at or before this request   */
+  KVC_PLAN_ROW_FULL = 2,   /* more than max_blocks * B tokens                    */
+  KVC_PLAN_INVALID = 3,    /* new_lens < -1 or kv_lens outside [0, max_blocks B] */
+  KVC_PLAN_TOKENS = 4      /* its tokens end beyond max_tokens                   */
+} kvc_plan_status;
+
+/* ---------------------------------------------------------------------------
+ * kvc_page_plan -- block tables, slots and positions of a step's new tokens.
+ *
+ * Request r holds kv_lens[r] tokens and brings new_lens[r] >= 0 new ones;
+ * new_lens[r] == -1 says that it is finished and returns its pages.
+ *   q_start[r]      sum of the new tokens before r (at most max_tokens);
+ *   kv_lens_out[r]  kv_lens[r] + new_lens[r]; 0 if finished;
+ *   block_table     the entries of pages that the new tokens begin, the rest
+ *                   untouched;
+ *   slot_map, positions [max_tokens]  slot and position of every new token, -1
+ *                   beyond the last one;
+ *   free_pages [P]  a stack of which the first *n_free entries are free.  The
+ *                   pages of finished requests are put on it in (request,
+ *                   block) order, then the new pages are taken from its top in
+ *                   (request, block) order; *n_free_out pages are left.
+ * A request that cannot be served is refused as a whole, with the reason in
+ * plan_status[r]: its length and table stay, its tokens keep their rows in
+ * the packed arrays and have slot and position -1.  Once the free pages ran
+ * out every later request that needs one is refused too.
+ * The state comes out in other buffers than it went in by (kv_lens_out,
+ * n_free_out): a call can be repeated with the same result.  No two buffers
+ * may overlap, except inputs that are only read.  At most 4,096 requests.
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_page_plan(const kvc_paged* pg, const int32_t* new_lens, const int32_t* kv_lens,
+                         int32_t* kv_lens_out, int32_t* block_table, int32_t* free_pages,
+                         const int32_t* n_free, int32_t* n_free_out, int32_t max_tokens,
+                         int32_t* q_start, int64_t* slot_map, int32_t* positions,
+                         int32_t* plan_status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_page_write -- put rows of K and V into their pages.
+ *
+ * src_K, src_V are views [n_src, n_layers, H, T, d]; token t of source r goes
+ * to slot_map[r * T + t] of layers [layer, layer + n_layers) of the pools.
+ * Tokens whose slot is outside [0, P B) are skipped.  New tokens of one layer,
+ * packed [N, H, d], are a view with n_src = n_layers = 1 and T = N; a chain's
+ * corrected caches [R, L, H, T, d] are views as they are.  Two tokens with the
+ * same slot race.  The pools may not overlap the sources.  n_layers * H <=
+ * 65,535.
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_page_write(const kvc_paged* pg, int32_t n_src, int32_t T, int32_t layer,
+                          int32_t n_layers, kvc_cache_view src_K, kvc_cache_view src_V,
+                          const int64_t* slot_map, kvc_cache_view pool_K, kvc_cache_view pool_V,
+                          cudaStream_t stream);
+
+/* Queries and outputs are [N, Hq, d] with d contiguous; strides in elements,
+ * multiples of 16 bytes. */
+typedef struct kvc_attn_params {
+  int32_t n_q_heads;    /* Hq, a multiple of H with Hq / H <= 64             */
+  int32_t n_tokens;     /* N rows of q, out and lse                          */
+  int32_t layer;        /* layer of the pools                                */
+  int32_t causal;       /* 1: a token sees keys up to its own position       */
+  int32_t window;       /* w > 0: of these only the last w; 0: all           */
+  float scale;          /* of the scores, finite and > 0                     */
+  int64_t q_s_tok, q_s_head;
+  int64_t out_s_tok, out_s_head;
+} kvc_attn_params;
+
+/* ---------------------------------------------------------------------------
+ * kvc_paged_attention -- attention of a chunk of new tokens over the paged
+ * cache.
+ *
+ * Query head h reads KV head h / (Hq / H).  Token i of request r, which
+ * brings n of them, has position p = kv_lens[r] - n + i (kv_lens counts the
+ * new tokens, whose keys are in the pages) and sees the keys j < kv_lens[r],
+ * with causal j <= p, with a window j > p - window:
+ *   out[row, h] = sum_j softmax_j(scale q . k_j) v_j,
+ *   lse[row, h] = log sum_j exp(scale q . k_j)         ([N, Hq] float32 or NULL).
+ * A row that sees no key gets out = 0 and lse = -inf.  Key and value rows at
+ * or beyond kv_lens[r] are never used, whatever they hold.  n == 1 is
+ * decoding; requests with one token, with many and with none may be mixed.
+ * Rows of no request are not written.  bf16 runs on tcgen05 tensor cores
+ * with fp32 softmax and accumulation (the probabilities are rounded to bf16
+ * for the product with V); f32 runs on FP32 FMA.
+ *
+ * `workspace` holds kvc_paged_attention_workspace() bytes (0 for descriptors
+ * that the call would refuse), 256-byte aligned.  ITS FIRST 8,192 BYTES MUST
+ * BE ZERO BEFORE ITS FIRST USE; every call leaves them zero.  Calls that may
+ * overlap on the GPU need workspaces of their own.  Results do not depend on
+ * the order in which CTAs finish.
+ *
+ * *dev_status becomes KVC_ERR_SHAPE if the lengths, q_start or a page index
+ * in use are out of range (lengths are clamped, the rows of such a page count
+ * as zeros), KVC_ERR_DEVICE_TIMEOUT if a bounded device wait expired (zero
+ * the workspace before its next use).
+ * ------------------------------------------------------------------------- */
+size_t kvc_paged_attention_workspace(const kvc_paged* pg, const kvc_attn_params* at);
+kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, const void* q,
+                               kvc_cache_view pool_K, kvc_cache_view pool_V,
+                               const int32_t* block_table, const int32_t* q_start,
+                               const int32_t* kv_lens, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
