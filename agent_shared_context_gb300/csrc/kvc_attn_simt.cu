@@ -1,5 +1,5 @@
-// kvc_attn_simt.cu -- attention of a chunk of new tokens over a paged cache in
-// FP32 arithmetic.
+// kvc_attn_simt.cu -- attention of a chunk of new tokens over a paged cache of
+// f32 keys and values, in FP32 arithmetic.
 //
 // One pass over the keys with the running maximum and sum of the softmax: with
 // x_j = scale log2(e) q.k_j, a row keeps m = max x_j, l = sum exp2(x_j - m) and
@@ -9,8 +9,6 @@
 //
 // A tile is 64 keys.  The rows of an item are (token, query head of the KV
 // head's group), so that K and V are read once for the whole group.
-#include <cuda_bf16.h>
-
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
 
@@ -28,30 +26,16 @@ __device__ __forceinline__ float4 load4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
 }
 
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&a);
-  u.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
 
 struct Smem {
   Shared sched;
   int32_t last;
 };
 
-// T: element type.  RPT: rows per thread; an item has 16 * RPT rows.  DC:
+// RPT: rows per thread; an item has 16 * RPT rows.  DC:
 // 64-column groups of d per thread.
-template <typename T, int RPT, int DC>
+template <int RPT, int DC>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, const SchedArgs sa) {
   extern __shared__ float4 smem4[];
   __shared__ Smem sh;
@@ -68,8 +52,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
   int32_t* counters = static_cast<int32_t*>(a.workspace);
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
   const size_t slot_n = slot_floats(kSlotRows, d);
-  const T* poolK = static_cast<const T*>(a.pool[0].base) + a.layer * a.pool[0].s_layer;
-  const T* poolV = static_cast<const T*>(a.pool[1].base) + a.layer * a.pool[1].s_layer;
+  const float* poolK = static_cast<const float*>(a.pool[0].base) + a.layer * a.pool[0].s_layer;
+  const float* poolV = static_cast<const float*>(a.pool[1].base) + a.layer * a.pool[1].s_layer;
 
   Item it;
   while (w.next(sa, &it)) {
@@ -80,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < rows) {
         const int tok = row / a.G, g = row - tok * a.G;
-        v = load4(static_cast<const T*>(a.q) + (it.q0 + tok) * a.q_tok +
+        v = load4(static_cast<const float*>(a.q) + (it.q0 + tok) * a.q_tok +
                   (it.h * a.G + g) * a.q_head + c);
       }
       *reinterpret_cast<float4*>(Qs + row * dp + c) = v;
@@ -219,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
         for (int c = 0; c < DC; ++c) {
           const int col = tx * 4 + c * 64;
           if (col < d)
-            store4(static_cast<T*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
+            store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
                    make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv,
                                o[i][c].w * inv));
         }
@@ -277,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
-      store4(static_cast<T*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
+      store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       if (a.lse != nullptr && col == 0)
         a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] =
@@ -286,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
   }
 }
 
-template <typename T, int RPT, int DC>
+template <int RPT, int DC>
 cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
@@ -294,7 +278,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   const int rows = 16 * RPT;
   const size_t smem = sizeof(float) * (static_cast<size_t>(rows) * (a.d + 4) + kTile * (a.d + 4) +
                                        kTile * a.d + rows * (kTile + 4));
-  auto* fn = attn_simt_kernel<T, RPT, DC>;
+  auto* fn = attn_simt_kernel<RPT, DC>;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -317,25 +301,24 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, int RPT>
+template <int RPT>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t stream) {
   switch ((a.d + 63) / 64) {
-    case 1: return launch_one<T, RPT, 1>(a, stream);
-    case 2: return launch_one<T, RPT, 2>(a, stream);
-    case 3: return launch_one<T, RPT, 3>(a, stream);
-    default: return launch_one<T, RPT, 4>(a, stream);
+    case 1: return launch_one<RPT, 1>(a, stream);
+    case 2: return launch_one<RPT, 2>(a, stream);
+    case 3: return launch_one<RPT, 3>(a, stream);
+    default: return launch_one<RPT, 4>(a, stream);
   }
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(kvc_dtype, int d, int) {
+size_t attn_simt_workspace_bytes(int d) {
   return kAttnCounterBytes + kMaxCtas * 2 * slot_floats(kSlotRows, d) * sizeof(float);
 }
 
-cudaError_t launch_attn_simt(const AttnArgs& a, kvc_dtype dtype, cudaStream_t stream) {
-  if (dtype == KVC_BF16) return launch_d<__nv_bfloat16, 4>(a, stream);
-  return launch_d<float, 4>(a, stream);
+cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t stream) {
+  return launch_d<4>(a, stream);
 }
 
 }  // namespace kvc

@@ -1,0 +1,968 @@
+// kvc_attn_tc.cu -- attention of a chunk of new tokens over a paged cache on
+// tcgen05 tensor cores (bf16, d = 64 or 128).
+//
+// The mathematics is that of kvc_attn_simt.cu: one pass over the keys with the
+// running maximum m and sum l of each row's softmax.  Any reference value that
+// keeps exp2(x - m) in range gives the same O / l, so m follows the maximum
+// only when a tile raises it by more than 8 (log2): P then stays below 2^8,
+// and O, which lives in TMEM, is rescaled in few tiles only.
+//
+// A row of the MMA is (token, query head of the KV head's group), so K and V
+// are read once for the whole group; a row tile holds floor(128 / G) tokens,
+// which one TMA box of Q fetches.  Two *streams* share a CTA, each with a row
+// tile's scores S (fp32, 128 columns) and output O in TMEM and a warpgroup for
+// its softmax, so the tensor core works for one while the other exponentiates:
+//   pair mode    (an item with more tokens than one row tile): the streams are
+//                two row tiles over the same key tiles;
+//   single mode  (decoding, the end of a chunk): both streams have the same
+//                rows and take every other key tile; stream 0 joins them.
+// Which mode an item takes is its own affair, so one launch serves batches
+// that mix decoding with chunks.  The work is divided over a persistent grid
+// as kvc_attn_sched.cuh says.
+//
+//   warps 0-3, 4-7  softmax of stream 0 and 1: scores from TMEM (thread = row),
+//                   running maximum, exp2, P to TMEM as bf16 (over S); the
+//                   output at the end of an item;
+//   warp 8          walks the share, hands the items to the others through a
+//                   ring, looks the pages up and issues the TMA loads of Q, K
+//                   and V;
+//   warp 9          issues S = Q K^T (both K-major in shared memory) and
+//                   O += P V (P in TMEM, V as the MN-major operand it is);
+//   warp 10         mends value tiles at the edge of sight (below).
+//
+// A key tile is 128 rows of a page, or as many whole pages (rounded up to 8
+// rows) as fit: pages of 8, 16, 32, 64 rows fill it, others leave holes that
+// are masked.  Where a tile is not in sight of all its rows the scores are
+// masked and warp 10 clears the value rows that no row sees, because 0 times
+// whatever the page holds there need not be 0.  A value row that some rows see
+// and others do not may hold an infinity or a NaN as well: it is cleared too,
+// and the rows that do see it add its products from memory.
+//
+// The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
+// 2^-8 average out over many keys of like weight but not where few carry a
+// row, so the remainder P - bf16(P) is multiplied too, in the steps of 16 keys
+// in which some row has a key with more than 1/8 of its sum so far (pair mode)
+// or in all (single mode, which waits for memory anyway): few steps of a long
+// context.  S leaves room for it in TMEM, beside P.
+//
+// Every wait is bounded: one that expires stores KVC_ERR_DEVICE_TIMEOUT into
+// *dev_status and raises the CTA's abort flag; the roles stop, copies and MMAs
+// in flight are waited for (with the limit again), TMEM is freed.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "kvc_attn_sched.cuh"
+#include "kvc_paged_internal.h"
+#include "kvc_ptx.cuh"
+
+namespace kvc {
+namespace {
+
+using namespace ptx;
+using namespace attn;
+
+constexpr int kThreads = 384;              // 12 warps (roles above, the last one idle)
+constexpr int kRegsSoftmax = 208;          // 256 threads x 208 + 128 x 88 = 384 x 168, the launch's
+constexpr int kRegsOther = 88;
+constexpr int kRowsM = 128;                // rows of a stream (MMA M)
+constexpr int kTile = 128;                 // keys of a tile
+constexpr int kSubBytes = kTile * 128;     // 128 rows x 64 bf16
+constexpr int kSlotRows = 256;             // rows of a partial result
+constexpr int kMaxCtas = 160;
+constexpr int kItems = 4;                  // depth of the item ring
+constexpr float kLag = 8.0f;               // log2 by which m may lag behind
+constexpr float kHeavy = 0.125f;           // share of a row's sum that makes a key heavy
+
+template <int D>
+struct Cfg {
+  static constexpr int kSub = D / 64;
+  static constexpr int kSlotBytes = kSub * kSubBytes;
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kQBytes = 2 * kSlotBytes;
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes;
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+
+struct TcArgs {
+  AttnArgs a;
+  SchedArgs s;
+  int32_t tok_tile;        // tokens of a row tile, floor(128 / G)
+  int32_t page_rows;       // rows of a page in a tile: B rounded up to 8, or 128
+  int32_t pages_tile;      // pages of a tile (1 if a page has 128 rows or more)
+  uint32_t holes[4];       // columns of a tile that never hold a key (pages < 128 rows)
+  int32_t has_holes;
+};
+
+struct ItemSlot {
+  Item it;
+  int32_t ring0;           // ring position of the item's first K tile
+};
+
+template <int NS>
+struct Bars {
+  uint64_t kv_full[NS], kv_raw[NS], kv_empty[NS];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t ml_full, ml_empty;      // stream 1's row statistics for stream 0
+  uint64_t wg[2];                  // the four warps of a stream
+  uint64_t drain;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+  int32_t last[2];
+  int32_t o_init[2];               // O holds something before the first P V
+  uint32_t heavy[2];               // steps of 16 keys with a remainder, a byte per warp
+  uint32_t poison[NS][4];          // cleared value rows that some rows of the item see
+  float ml[kRowsM][2];
+  ItemSlot items[kItems];
+  Shared sched;
+};
+
+template <int NS>
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Bars<NS>* b,
+                                              int32_t* dev_status) {
+  if (mbar_wait_bounded(bar, parity, kWaitLimitNs, &b->abort_flag)) return true;
+  volatile int32_t* ab = &b->abort_flag;
+  if (*ab == 0) {
+    *ab = 1;
+    atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_DEVICE_TIMEOUT));
+  }
+  return false;
+}
+
+// The same for a whole warp: all lanes give up together.
+template <int NS>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b,
+                                          int32_t* dev_status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, b, dev_status));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+
+// ------------------------------------------------------------ tile geometry
+// Ring positions, relative to the item's first: the order in which the MMAs
+// consume the tiles.
+__device__ __forceinline__ int ring_k(bool pair, int i) {
+  return pair ? 2 * i : (i < 2 ? i : 2 * i - 1);
+}
+__device__ __forceinline__ int ring_v(bool pair, int n, int i) {
+  return pair ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 + 2 * i);
+}
+
+struct TileSpan {
+  int tok0, cnt;           // first key token and tokens of the tile
+};
+
+__device__ __forceinline__ TileSpan tile_span(const TcArgs& p, int tile) {
+  TileSpan t;
+  const int g = tile / p.s.group_tiles, sub = tile - g * p.s.group_tiles;
+  t.tok0 = g * p.s.group_tok + sub * p.s.tile_tok;
+  t.cnt = min(p.s.tile_tok, p.s.group_tok - sub * p.s.tile_tok);
+  return t;
+}
+
+// Column of the tile at which token `tok` lies or would lie: the keys before it
+// are exactly the key columns below.
+__device__ __forceinline__ int tile_col(const TcArgs& p, const TileSpan& t, int tok) {
+  const int rel = tok - t.tok0;
+  if (rel <= 0) return 0;
+  if (rel >= t.cnt) return kTile;
+  if (p.pages_tile == 1) return rel;
+  const int pg = rel / p.a.B;
+  return pg * p.page_rows + (rel - pg * p.a.B);
+}
+
+// Token of a key column (not of a hole).
+__device__ __forceinline__ int tile_tok(const TcArgs& p, const TileSpan& t, int col) {
+  if (p.pages_tile == 1) return t.tok0 + col;
+  const int pg = col / p.page_rows;
+  return t.tok0 + pg * p.a.B + (col - pg * p.page_rows);
+}
+
+// Keys that every row of tokens [pos0, pos0 + nt) sees, and that any sees.
+struct Sight {
+  int all_lo, all_hi, any_lo, any_hi;
+};
+
+__device__ __forceinline__ Sight sight(const AttnArgs& a, int kv, int pos0, int nt) {
+  Sight s;
+  s.all_hi = a.causal ? min(kv, pos0 + 1) : kv;
+  s.any_hi = a.causal ? min(kv, pos0 + nt) : kv;
+  s.all_lo = a.window > 0 ? max(0, pos0 + nt - a.window) : 0;
+  s.any_lo = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
+  return s;
+}
+
+// Whether the tile's value rows need mending before the product.
+__device__ __forceinline__ bool at_edge(const TileSpan& t, const Sight& s) {
+  return t.tok0 + t.cnt > s.all_hi || t.tok0 < s.all_lo;
+}
+
+__device__ __forceinline__ uint32_t bits_below(int n) {      // n lowest bits
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs p) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kSlots;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsM, kTile);
+  constexpr uint32_t kIdescO = idesc_bf16_f32(kRowsM, D) | kIdescBMnMajor;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars<NS> bars_mem;
+  Bars<NS>* b = &bars_mem;
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_smem = smem;
+  uint8_t* kv_smem = smem + C::kQBytes;
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&b->kv_full[i], 1);
+      mbar_init(&b->kv_raw[i], 1);
+      mbar_init(&b->kv_empty[i], 1);
+    }
+    mbar_init(&b->q_full, 1);
+    mbar_init(&b->q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b->s_full[i], 1);
+      mbar_init(&b->p_full[i], 4);
+      mbar_init(&b->wg[i], 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&b->item_full[i], 1);
+      mbar_init(&b->item_empty[i], 10);    // 8 softmax warps, the MMA and the mending warp
+    }
+    mbar_init(&b->ml_full, 4);
+    mbar_init(&b->ml_empty, 4);
+    mbar_init(&b->drain, 1);
+    b->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc<512>(&b->tmem_base);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (p.pages_tile * p.page_rows < kTile) {
+    // rows that no load ever writes: 0, so that P V is 0 there
+    uint4* z = reinterpret_cast<uint4*>(kv_smem);
+    for (int i = threadIdx.x; i < NS * C::kSlotBytes / 16; i += kThreads)
+      z[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  Walker w = walker_begin<kThreads>(p.s, &b->sched, a.dev_status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = b->tmem_base;
+  const uint32_t tS[2] = {tmem, tmem + 128};
+  const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    regs_lower<kRegsOther>();
+    int ring = 0, n_items = 0;
+    bool ok = true;
+    uint32_t raw_phase = 0;                       // bit i: parity of kv_raw[i]'s next phase
+    uint32_t raw_open = 0;                        // bit i: slot i's last load went to kv_raw
+    const int boxes = p.pages_tile * C::kSub;
+    const int my_page = lane / C::kSub, my_sub = lane - my_page * C::kSub;
+    const uint32_t tile_bytes = static_cast<uint32_t>(p.pages_tile * p.page_rows) * 128 * C::kSub;
+    bool bad_page = false;
+
+    for (;;) {
+      Item it;
+      const bool more = w.next(p.s, &it);
+      const int slot = n_items % kItems;
+      ok = warp_wait(&b->item_empty[slot], ((n_items / kItems) & 1) ^ 1, b, a.dev_status);
+      if (!ok) break;
+      if (!more) it.ntiles = 0;
+      if (lane == 0) {
+        b->items[slot].it = it;
+        b->items[slot].ring0 = ring;
+        mbar_arrive(&b->item_full[slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+      const bool pair = it.nt > p.tok_tile;
+      const Sight see = sight(a, it.kv, it.pos0, it.nt);
+
+      // Q: one box per row tile and 64 columns
+      ok = warp_wait(&b->q_empty, (n_items & 1) ^ 1, b, a.dev_status);
+      if (!ok) break;
+      if (lane == 0) {
+        const int tiles = pair ? 2 : 1;
+        mbar_arrive_expect_tx(&b->q_full,
+                              static_cast<uint32_t>(tiles * C::kSub * a.G * p.tok_tile) * 128);
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < C::kSub; ++c)
+            tma_load_3d(q_smem + (t * C::kSub + c) * kSubBytes, &maps.q, &b->q_full, c * 64,
+                        it.h * a.G, it.q0 + t * p.tok_tile);
+      }
+      ++n_items;
+
+      auto load = [&](int kv, int i) -> bool {
+        const int s = ring % NS;
+        if (!warp_wait(&b->kv_empty[s], ((ring / NS) & 1) ^ 1, b, a.dev_status)) return false;
+        const int tile = it.tile0 + i;
+        const int g = tile / p.s.group_tiles;
+        uint64_t* bar = &b->kv_full[s];
+        raw_open &= ~(1u << s);
+        if (kv == 1 && at_edge(tile_span(p, tile), see)) {
+          bar = &b->kv_raw[s];
+          raw_open |= 1u << s;
+          raw_phase ^= 1u << s;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int blk = p.pages_tile == 1 ? g : g * p.pages_tile + my_page;
+          const int row = p.pages_tile == 1 ? (tile - g * p.s.group_tiles) * kTile : 0;
+          int page = a.P;                          // beyond the pool: the box is filled with 0
+          if (static_cast<int64_t>(blk) * a.B < it.kv) {
+            page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
+            if (page < 0 || page >= a.P) {
+              page = a.P;
+              bad_page = true;
+            }
+          }
+          tma_load_5d(kv_smem + s * C::kSlotBytes + my_sub * kSubBytes +
+                          my_page * p.page_rows * 128,
+                      kv == 0 ? &maps.k : &maps.v, bar, my_sub * 64, row, it.h, a.layer, page);
+        }
+        __syncwarp();
+        ++ring;
+        return true;
+      };
+      const int n = it.ntiles;
+      if (pair) {
+        for (int i = 0; i < n && ok; ++i) ok = load(0, i) && load(1, i);
+      } else {
+        ok = load(0, 0);
+        if (ok && n > 1) ok = load(0, 1);
+        for (int i = 0; i < n && ok; ++i) {
+          ok = load(1, i);
+          if (ok && i + 2 < n) ok = load(0, i + 2);
+        }
+      }
+      if (!ok) break;
+    }
+    if (bad_page) atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
+    if (!ok) {
+      // the copies in flight write to this CTA's shared memory: let them land
+      for (int i = ring - 1; i >= 0 && i >= ring - NS; --i) {
+        const int s = i % NS;
+        if ((raw_open >> s) & 1)
+          mbar_wait_bounded(&b->kv_raw[s], ((raw_phase >> s) & 1) ^ 1, kWaitLimitNs);
+        else
+          mbar_wait_bounded(&b->kv_full[s], (i / NS) & 1, kWaitLimitNs);
+      }
+      if (n_items > 0) mbar_wait_bounded(&b->q_full, (n_items - 1) & 1, kWaitLimitNs);
+    }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------------- MMA
+    regs_lower<kRegsOther>();
+    if (lane == 0) {
+      uint32_t ph_p[2] = {0, 0};
+      bool ok = true;
+      for (int n_items = 0; ok; ++n_items) {
+        const int slot = n_items % kItems;
+        ok = wait_or_abort(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+        if (!ok) break;
+        const int n = b->items[slot].it.ntiles;
+        if (n == 0) break;
+        const bool pair = b->items[slot].it.nt > p.tok_tile;
+        const int ring0 = b->items[slot].ring0;
+        mbar_arrive(&b->item_empty[slot]);
+
+        auto full = [&](int pos) {
+          return wait_or_abort(&b->kv_full[pos % NS], (pos / NS) & 1, b, a.dev_status);
+        };
+        auto qk = [&](int st, int pos) {
+          const uint32_t qa = smem_u32(q_smem + (pair ? st : 0) * C::kSlotBytes);
+          const uint32_t ka = smem_u32(kv_smem + (pos % NS) * C::kSlotBytes);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * kSubBytes + (k % 4) * 32;
+            mma_bf16_ss(tS[st], desc_kmajor_sw128(qa + off), desc_kmajor_sw128(ka + off), kIdescS,
+                        k > 0);
+          }
+        };
+        auto pv = [&](int st, int pos, bool acc) {
+          const uint32_t va = smem_u32(kv_smem + (pos % NS) * C::kSlotBytes);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16_ts(tO[st], tS[st] + k * 8, desc_mnmajor_sw128(va + k * 2048, kSubBytes),
+                        kIdescO, acc || k > 0);
+          uint32_t rest = *static_cast<volatile uint32_t*>(&b->heavy[st]);
+          rest |= rest >> 16;
+          rest = (rest | rest >> 8) & 0xffu;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            if ((rest >> k) & 1u)
+              mma_bf16_ts(tO[st], tS[st] + 64 + k * 8, desc_mnmajor_sw128(va + k * 2048, kSubBytes),
+                          kIdescO, 1);
+        };
+        auto probs = [&](int st) {                 // stream st's P is in TMEM
+          if (!wait_or_abort(&b->p_full[st], ph_p[st], b, a.dev_status)) return false;
+          ph_p[st] ^= 1;
+          tc_fence_after();
+          return true;
+        };
+        ok = wait_or_abort(&b->q_full, n_items & 1, b, a.dev_status);
+        if (!ok) break;
+        tc_fence_after();
+        if (pair) {
+          ok = full(ring0);
+          if (!ok) break;
+          qk(0, ring0);
+          mma_commit(&b->s_full[0]);
+          qk(1, ring0);
+          mma_commit(&b->s_full[1]);
+          mma_commit(&b->kv_empty[ring0 % NS]);
+          if (n == 1) mma_commit(&b->q_empty);
+          for (int j = 0; j < n && ok; ++j) {
+            const int pv_at = ring0 + 2 * j + 1, k_at = pv_at + 1;
+            const bool more = j + 1 < n;
+            ok = full(pv_at) && probs(0);
+            if (!ok) break;
+            pv(0, pv_at, j > 0 || b->o_init[0]);
+            if (more) {
+              ok = full(k_at);
+              if (!ok) break;
+              qk(0, k_at);
+            }
+            mma_commit(&b->s_full[0]);
+            ok = probs(1);
+            if (!ok) break;
+            pv(1, pv_at, j > 0 || b->o_init[1]);
+            mma_commit(&b->kv_empty[pv_at % NS]);
+            if (more) {
+              qk(1, k_at);
+              mma_commit(&b->kv_empty[k_at % NS]);
+              if (j + 2 == n) mma_commit(&b->q_empty);
+            }
+            mma_commit(&b->s_full[1]);
+          }
+        } else {
+          for (int i = 0; i < 2 && i < n && ok; ++i) {
+            ok = full(ring0 + i);
+            if (!ok) break;
+            qk(i, ring0 + i);
+            mma_commit(&b->s_full[i]);
+            mma_commit(&b->kv_empty[(ring0 + i) % NS]);
+          }
+          if (n <= 2) mma_commit(&b->q_empty);
+          for (int i = 0; i < n && ok; ++i) {
+            const int st = i & 1, v_at = ring0 + ring_v(false, n, i);
+            ok = full(v_at) && probs(st);
+            if (!ok) break;
+            pv(st, v_at, i >= 2 || b->o_init[st]);
+            mma_commit(&b->kv_empty[v_at % NS]);
+            if (i + 2 < n) {
+              const int k_at = ring0 + ring_k(false, i + 2);
+              ok = full(k_at);
+              if (!ok) break;
+              qk(st, k_at);
+              mma_commit(&b->kv_empty[k_at % NS]);
+              if (i + 3 == n) mma_commit(&b->q_empty);
+            }
+            mma_commit(&b->s_full[st]);
+          }
+        }
+      }
+      if (!ok) {
+        mma_commit(&b->drain);
+        mbar_wait_bounded(&b->drain, 0, kWaitLimitNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------- value tiles at an edge
+    regs_lower<kRegsOther>();
+    uint32_t raw_phase = 0;
+    bool ok = true;
+    for (int n_items = 0; ok; ++n_items) {
+      const int slot = n_items % kItems;
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      if (!ok) break;
+      const Item it = b->items[slot].it;
+      const int ring0 = b->items[slot].ring0;
+      __syncwarp();
+      if (it.ntiles == 0) break;
+      if (lane == 0) mbar_arrive(&b->item_empty[slot]);
+      const bool pair = it.nt > p.tok_tile;
+      const Sight see = sight(a, it.kv, it.pos0, it.nt);
+      for (int i = 0; i < it.ntiles && ok; ++i) {
+        const TileSpan t = tile_span(p, it.tile0 + i);
+        if (!at_edge(t, see)) continue;
+        const int s = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
+        ok = warp_wait(&b->kv_raw[s], (raw_phase >> s) & 1, b, a.dev_status);
+        if (!ok) break;
+        raw_phase ^= 1u << s;
+        const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
+        const int c1 = tile_col(p, t, see.all_lo), c2 = tile_col(p, t, see.all_hi);
+        uint8_t* rows = kv_smem + s * C::kSlotBytes;
+        uint32_t found[4] = {0, 0, 0, 0};
+        // lanes 0 .. 8 kSub - 1 hold a row, 16 bytes each
+        constexpr int kLanes = 8 * C::kSub, kPer = 32 / kLanes;
+        const int sub = (lane % kLanes) / 8, unit = lane % 8;
+#pragma unroll 4
+        for (int n0 = 0; n0 < kTile; n0 += kPer) {
+          const int n = n0 + lane / kLanes;
+          uint4* at = reinterpret_cast<uint4*>(rows + sub * kSubBytes + n * 128 + unit * 16);
+          const bool dark = n < c0 || n >= c3;              // no row sees it
+          bool clear = dark;
+          if (!dark && (n < c1 || n >= c2)) {               // some rows see it
+            const uint4 x = *at;
+            auto odd = [](uint32_t u) {
+              return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+            };
+            clear = odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w);
+          }
+          const uint32_t who = __ballot_sync(0xffffffffu, clear);
+          const int first = lane / kLanes * kLanes;
+          const bool row_clear = ((who >> first) & bits_below(kLanes)) != 0;
+          if (row_clear) *at = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (n0 + j >= c0 && n0 + j < c3 && ((who >> (j * kLanes)) & bits_below(kLanes)))
+              found[(n0 + j) >> 5] |= 1u << ((n0 + j) & 31);
+        }
+        if (lane < 4)
+          b->poison[s][lane] = lane == 0 ? found[0] : lane == 1 ? found[1] : lane == 2 ? found[2]
+                                                                                    : found[3];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->kv_full[s]);
+      }
+    }
+  } else if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    regs_raise<kRegsSoftmax>();
+    const int st = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;    // lane 32 w in bits 31-16
+    const uint32_t sS = tS[st] + lane_base, sO = tO[st] + lane_base;
+    const int row_tok = row / a.G, row_g = row - row_tok * a.G;
+    const bool row_in_tile = row_tok < p.tok_tile;
+    uint32_t ph_s = 0, ph_wg = 0, ph_ml = 0;
+    int32_t* counters = static_cast<int32_t*>(a.workspace);
+    float* slots =
+        reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
+    const size_t slot_n = slot_floats(kSlotRows, D);
+    bool ok = true;
+
+    for (int n_items = 0; ok; ++n_items) {
+      const int slot = n_items % kItems;
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      if (!ok) break;
+      const Item it = b->items[slot].it;
+      const int ring0 = b->items[slot].ring0;
+      __syncwarp();
+      if (it.ntiles == 0) break;
+      if (lane == 0) mbar_arrive(&b->item_empty[slot]);
+      const bool pair = it.nt > p.tok_tile;
+      const int n_st = pair ? it.ntiles : (it.ntiles + 1 - st) >> 1;
+      const int tok_off = pair ? st * p.tok_tile : 0;       // first token of the stream's rows
+      const int n_tok = min(p.tok_tile, it.nt - tok_off);
+      const bool valid = row_in_tile && row_tok < n_tok;
+      const bool busy = (warp & 3) * 32 < n_tok * a.G;      // any valid row in the warp
+      const Sight see = sight(a, it.kv, it.pos0 + tok_off, n_tok);
+      const Sight see_item = sight(a, it.kv, it.pos0, it.nt);
+      const int pos = it.pos0 + tok_off + min(row_tok, n_tok - 1);
+      const int key_hi = a.causal ? min(it.kv, pos + 1) : it.kv;
+      const int key_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+
+      for (int k = 0; k < n_st; ++k) {
+        const int i = pair ? k : 2 * k + st;                // key tile of the item
+        ok = warp_wait(&b->s_full[st], ph_s, b, a.dev_status);
+        if (!ok) break;
+        ph_s ^= 1;
+        if (busy) {
+          tc_fence_after();
+          uint32_t x[kTile];
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) tmem_ld_32x32b_x32(sS + c, x + c);
+          tmem_ld_wait();
+          const TileSpan t = tile_span(p, it.tile0 + i);
+          const bool whole = !p.has_holes && t.cnt == kTile && t.tok0 >= see.all_lo &&
+                             t.tok0 + kTile <= see.all_hi;
+          if (!whole) {
+            const int lo = tile_col(p, t, key_lo), hi = min(tile_col(p, t, key_hi),
+                                                            p.pages_tile == 1 ? t.cnt : kTile);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t keep =
+                  bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) & ~p.holes[c];
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((keep >> j) & 1u)) x[32 * c + j] = 0xff800000u;      // -inf
+            }
+          }
+          float mx[8];                                       // of each 16 keys
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            mx[g] = __uint_as_float(x[16 * g]);
+#pragma unroll
+            for (int j = 1; j < 16; ++j) mx[g] = fmaxf(mx[g], __uint_as_float(x[16 * g + j]));
+          }
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+                            a.scale_log2;
+          const bool raise = top > m + kLag || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise ? exp2_fast(m - top) : 1.f;              // 0 from m = -inf
+            if (raise) m = top;
+            l *= f;
+            if (k > 0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(sO + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st_32x32b_x32(sO + c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          // steps in which a key has more than kHeavy of the row's sum so far
+          uint32_t heavy = 0xffu;
+          if (pair) {
+            const float least = __log2f(kHeavy * (l + exp2_fast(top - ref)));
+            heavy = 0;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              if (__any_sync(0xffffffffu, valid && fmaf(mx[g], a.scale_log2, -ref) > least))
+                heavy |= 1u << g;
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            uint32_t rest[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int e = 16 * g + 2 * j;
+              const float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), a.scale_log2, -ref));
+              const float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), a.scale_log2, -ref));
+              sum[j & 3] += p0 + p1;
+              const uint32_t u = pack_bf16(p0, p1);
+              x[e >> 1] = u;
+              rest[j] = 0;
+              if ((heavy >> g) & 1u)
+                rest[j] = pack_bf16(p0 - __uint_as_float(u << 16),
+                                    p1 - __uint_as_float(u & 0xffff0000u));
+            }
+            tmem_st_32x32b_x8(sS + 64 + 8 * g, rest);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_32x32b_x32(sS, x);
+          tmem_st_32x32b_x32(sS + 32, x + 32);
+          if (lane == 0) reinterpret_cast<volatile uint8_t*>(&b->heavy[st])[warp & 3] = heavy;
+          tmem_st_wait();
+
+          bool init = false;
+          if (at_edge(t, see_item)) {
+            // rare: value rows that were cleared although some rows see them
+            const int pos_v = ring0 + ring_v(pair, it.ntiles, i);
+            ok = warp_wait(&b->kv_full[pos_v % NS], (pos_v / NS) & 1, b, a.dev_status);
+            if (!ok) break;
+            for (int n = 0; n < kTile; ++n) {
+              if (!((b->poison[pos_v % NS][n >> 5] >> (n & 31)) & 1u)) continue;
+              const int tok = tile_tok(p, t, n), blk = tok / a.B;
+              const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
+              const uint32_t two = tmem_ld_32x32b_x1(sS + (n >> 1));
+              tmem_ld_wait();
+              const float pr = __uint_as_float((n & 1) ? two & 0xffff0000u : two << 16);
+              const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool[1].base) +
+                                       page * a.pool[1].s_req + a.layer * a.pool[1].s_layer +
+                                       it.h * a.pool[1].s_head +
+                                       static_cast<int64_t>(tok - blk * a.B) * a.pool[1].s_tok;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(sO + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const float old = k > 0 || init ? __uint_as_float(o[j]) : 0.f;
+                  const float add = pr == 0.f ? 0.f : pr * __bfloat162float(v[c + j]);
+                  o[j] = __float_as_uint(old + add);
+                }
+                tmem_st_32x32b_x32(sO + c, o);
+                tmem_st_wait();
+              }
+              init = true;
+            }
+          }
+          if (k == 0 && (warp & 3) == 0 && lane == 0) b->o_init[st] = init ? 1 : 0;
+          tc_fence_before();
+        } else if (lane == 0) {
+          reinterpret_cast<volatile uint8_t*>(&b->heavy[st])[warp & 3] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->p_full[st]);
+      }
+      if (!ok) break;
+      if (n_st > 0) {
+        ok = warp_wait(&b->s_full[st], ph_s, b, a.dev_status);      // O is complete
+        if (!ok) break;
+        ph_s ^= 1;
+        tc_fence_after();
+      }
+
+      // single mode: stream 0 joins the two streams' rows
+      float f0 = 1.f, f1 = 0.f;
+      const bool join = !pair && it.ntiles > 1;
+      if (join) {
+        if (st == 1) {
+          b->ml[row][0] = m;
+          b->ml[row][1] = l;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->ml_full);
+          ok = warp_wait(&b->ml_empty, ph_ml, b, a.dev_status);
+          if (!ok) break;
+          ph_ml ^= 1;
+          continue;
+        }
+        ok = warp_wait(&b->ml_full, ph_ml, b, a.dev_status);
+        if (!ok) break;
+        ph_ml ^= 1;
+        tc_fence_after();
+        const float m1 = b->ml[row][0], l1 = b->ml[row][1];
+        const float top = fmaxf(m, m1);
+        f0 = part_weight(m, l, top);
+        f1 = part_weight(m1, l1, top);
+        l = l * f0 + l1 * f1;
+        m = top;
+      } else if (!pair && st == 1) {
+        continue;
+      }
+      const bool whole_item = it.nparts == 1;
+      const float inv = whole_item ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const int head = it.h * a.G + row_g;
+      const int64_t q_row = it.q0 + tok_off + row_tok;
+      const int slot_row = (pair ? st * kRowsM : 0) + row;
+      float* part = slots + (static_cast<size_t>(blockIdx.x) * 2 + slot_of(it.part)) * slot_n;
+      if (busy) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + q_row * a.o_tok + head * a.o_head;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(sO + c, o);
+          tmem_ld_wait();
+          if (join) {
+            uint32_t o1[32];
+            tmem_ld_32x32b_x32(tO[1] + lane_base + c, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float u = f0 == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
+              const float v = f1 == 0.f ? 0.f : __uint_as_float(o1[j]) * f1;
+              o[j] = __float_as_uint(u + v);
+            }
+          }
+          if (valid && whole_item) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 u;
+              const float* f = reinterpret_cast<const float*>(o + j);
+              u.x = pack_bf16(l == 0.f ? 0.f : f[0] * inv, l == 0.f ? 0.f : f[1] * inv);
+              u.y = pack_bf16(l == 0.f ? 0.f : f[2] * inv, l == 0.f ? 0.f : f[3] * inv);
+              u.z = pack_bf16(l == 0.f ? 0.f : f[4] * inv, l == 0.f ? 0.f : f[5] * inv);
+              u.w = pack_bf16(l == 0.f ? 0.f : f[6] * inv, l == 0.f ? 0.f : f[7] * inv);
+              *reinterpret_cast<uint4*>(out + c + j) = u;
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(part + slot_row * D + c + j) =
+                  make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+        tc_fence_before();
+        if (valid && whole_item && a.lse != nullptr)
+          a.lse[q_row * (a.H * a.G) + head] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (valid && !whole_item) {
+          part[kSlotRows * D + slot_row] = m;
+          part[kSlotRows * D + kSlotRows + slot_row] = l;
+        }
+      }
+      __syncwarp();
+      if (join && lane == 0) mbar_arrive(&b->ml_empty);
+      if (whole_item) continue;
+
+      // a divided item: join the parts if all others have left theirs
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->wg[st]);
+      ok = warp_wait(&b->wg[st], ph_wg, b, a.dev_status);
+      if (!ok) break;
+      ph_wg ^= 1;
+      if (row == 0) {
+        __threadfence();
+        b->last[st] = atomicAdd(counters + 2 * it.cta0 + st, 1) == it.nparts - 1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->wg[st]);
+      ok = warp_wait(&b->wg[st], ph_wg, b, a.dev_status);
+      if (!ok) break;
+      ph_wg ^= 1;
+      if (!b->last[st]) continue;
+      __threadfence();
+      if (row == 0) counters[2 * it.cta0 + st] = 0;
+      const int rows = n_tok * a.G, base = pair ? st * kRowsM : 0;
+      constexpr int kDv = D / 4;
+      for (int e = row; e < rows * kDv; e += 128) {
+        const int er = e / kDv, col = (e - er * kDv) * 4;
+        float M = -INFINITY;
+        for (int q = 0; q < it.nparts; ++q) {
+          const float* ps = slots + (static_cast<size_t>(it.cta0 + q) * 2 + slot_of(q)) * slot_n;
+          M = fmaxf(M, __ldcg(ps + kSlotRows * D + base + er));
+        }
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < it.nparts; ++q) {
+          const float* ps = slots + (static_cast<size_t>(it.cta0 + q) * 2 + slot_of(q)) * slot_n;
+          const float pm = __ldcg(ps + kSlotRows * D + base + er);
+          const float pl = __ldcg(ps + kSlotRows * D + kSlotRows + base + er);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + (base + er) * D + col));
+          if (pl == 0.f) continue;
+          const float f = part_weight(pm, pl, M);
+          L = fmaf(pl, f, L);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
+        const float r = 1.f / L;
+        const int tok = er / a.G, hd = it.h * a.G + er - tok * a.G;
+        const int64_t orow = it.q0 + tok_off + tok;
+        uint2 u = make_uint2(0, 0);
+        if (L != 0.f) {
+          u.x = pack_bf16(acc.x * r, acc.y * r);
+          u.y = pack_bf16(acc.z * r, acc.w * r);
+        }
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.o_tok +
+                                  hd * a.o_head + col) = u;
+        if (a.lse != nullptr && col == 0)
+          a.lse[orow * (a.H * a.G) + hd] =
+              L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      }
+    }
+  } else {
+    regs_lower<kRegsOther>();                     // a warpgroup moves its registers together
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc<512>(tmem);
+}
+
+cudaError_t encode_pool(CUtensorMap* map, const AttnArgs& a, int kv, int rows) {
+  const View& v = a.pool[kv];
+  const int64_t ext[4] = {a.B, a.H, a.L, a.P};
+  const int64_t str[4] = {v.s_tok, v.s_head, v.s_layer, v.s_req};
+  uint64_t dims[5] = {static_cast<uint64_t>(a.d), 0, 0, 0, 0}, strides[4];
+  for (int i = 0; i < 4; ++i) {
+    dims[i + 1] = static_cast<uint64_t>(ext[i]);
+    strides[i] = static_cast<uint64_t>(ext[i] > 1 ? str[i] : a.d) * 2;   // unused where 1 long
+  }
+  const uint32_t box[5] = {64, static_cast<uint32_t>(rows), 1, 1, 1};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, v.base, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D>
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  TcArgs p;
+  std::memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.tok_tile = kRowsM / a.G;
+  p.page_rows = a.B < kTile ? (a.B + 7) / 8 * 8 : kTile;
+  p.pages_tile = a.B < kTile ? kTile / p.page_rows : 1;
+  if (a.B < kTile)
+    for (int n = 0; n < kTile; ++n)
+      if (n / p.page_rows >= p.pages_tile || n % p.page_rows >= a.B) p.holes[n >> 5] |= 1u << (n & 31);
+  p.has_holes = (p.holes[0] | p.holes[1] | p.holes[2] | p.holes[3]) != 0;
+  SchedArgs& s = p.s;
+  s.q_start = a.q_start;
+  s.kv_lens = a.kv_lens;
+  s.R = a.R;
+  s.H = a.H;
+  s.N = a.N;
+  s.kv_cap = a.width * a.B;
+  s.causal = a.causal;
+  s.window = a.window;
+  s.tok_item = 2 * p.tok_tile;
+  s.group_tok = a.B < kTile ? p.pages_tile * a.B : a.B;
+  s.group_tiles = a.B < kTile ? 1 : (a.B + kTile - 1) / kTile;
+  s.tile_tok = a.B < kTile ? s.group_tok : kTile;
+
+  TcMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  {
+    const int hq = a.H * a.G;
+    const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(hq),
+                              static_cast<uint64_t>(a.N)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(hq > 1 ? a.q_head : D) * 2,
+                                 static_cast<uint64_t>(a.N > 1 ? a.q_tok : D) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(p.tok_tile)};
+    e = encode_tiled(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims,
+                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
+  e = encode_pool(&maps.k, a, 0, p.page_rows);
+  if (e != cudaSuccess) return e;
+  e = encode_pool(&maps.v, a, 1, p.page_rows);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
+  attn_tc_kernel<D><<<grid, kThreads, Cfg<D>::kSmem, stream>>>(maps, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tc_workspace_bytes(int d) {
+  return kAttnCounterBytes + kMaxCtas * 2 * slot_floats(kSlotRows, d) * sizeof(float);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? launch_tc<128>(a, stream) : launch_tc<64>(a, stream);
+}
+
+}  // namespace kvc

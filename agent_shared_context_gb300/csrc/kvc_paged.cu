@@ -91,6 +91,14 @@ kvc_status check_view(const kvc_paged* pg, const kvc_cache_view& v, const char* 
   return KVC_OK;
 }
 
+kvc_status check_pool(const kvc_paged* pg, const kvc_cache_view& v, const char* name) {
+  KVC_TRY(check_view(pg, v, name));
+  if ((pg->n_pages > 1 && v.s_req < pg->d) || (pg->L > 1 && v.s_layer < pg->d) ||
+      (pg->H > 1 && v.s_head < pg->d))
+    return fail(KVC_ERR_SHAPE, "%s: strides of a pool must be >= d", name);
+  return KVC_OK;
+}
+
 Span view_span(const kvc_paged* pg, const kvc_cache_view& v, int64_t R, int64_t L, int64_t T) {
   const int64_t last = (R - 1) * v.s_req + (L - 1) * v.s_layer + (pg->H - 1) * v.s_head +
                        (T - 1) * v.s_tok + pg->d;
@@ -122,8 +130,9 @@ kvc_status check_rows(const kvc_paged* pg, const kvc_attn_params* at, const void
                       int64_t s_head, const char* name) {
   KVC_TRY(check_ptr(p, name, 16));
   const int64_t e = elem_bytes(pg->dtype), lim = (int64_t(1) << 40) / e;
-  if (s_tok < 0 || (at->n_q_heads > 1 && s_head < pg->d) || s_head < 0)
-    return fail(KVC_ERR_SHAPE, "%s: strides must be >= 0 and the head stride >= d", name);
+  if (s_tok < 0 || s_head < 0 || (at->n_q_heads > 1 && s_head < pg->d) ||
+      (at->n_tokens > 1 && s_tok < pg->d))
+    return fail(KVC_ERR_SHAPE, "%s: strides must be >= d", name);
   if (s_tok >= lim || s_head >= lim)
     return fail(KVC_ERR_UNSUPPORTED, "%s: byte strides must be < 2^40", name);
   if ((s_tok * e) % 16 || (s_head * e) % 16)
@@ -136,6 +145,10 @@ Span rows_span(const kvc_paged* pg, const kvc_attn_params* at, const void* p, in
   const int64_t last =
       (at->n_tokens - 1) * s_tok + (at->n_q_heads - 1) * s_head + pg->d;
   return span(p, last * elem_bytes(pg->dtype));
+}
+
+size_t attn_workspace_bytes(const kvc_paged* pg) {
+  return pg->dtype == KVC_BF16 ? attn_tc_workspace_bytes(pg->d) : attn_simt_workspace_bytes(pg->d);
 }
 
 }  // namespace
@@ -230,8 +243,8 @@ kvc_status kvc_page_write(const kvc_paged* pg, int32_t n_src, int32_t T, int32_t
                 static_cast<long long>(n_layers) * pg->H);
   KVC_TRY(check_view(pg, src_K, "src_K"));
   KVC_TRY(check_view(pg, src_V, "src_V"));
-  KVC_TRY(check_view(pg, pool_K, "pool_K"));
-  KVC_TRY(check_view(pg, pool_V, "pool_V"));
+  KVC_TRY(check_pool(pg, pool_K, "pool_K"));
+  KVC_TRY(check_pool(pg, pool_V, "pool_V"));
   if (n_src == 0 || T == 0) return KVC_OK;
   KVC_TRY(check_ptr(slot_map, "slot_map", 8));
   const Span pools[2] = {view_span(pg, pool_K, pg->n_pages, pg->L, pg->page_size),
@@ -266,7 +279,7 @@ kvc_status kvc_page_write(const kvc_paged* pg, int32_t n_src, int32_t T, int32_t
 size_t kvc_paged_attention_workspace(const kvc_paged* pg, const kvc_attn_params* at) {
   if (check_paged(pg) != KVC_OK || check_head_dim(pg) != KVC_OK || check_attn(pg, at) != KVC_OK)
     return 0;
-  return attn_workspace_bytes(pg->dtype, pg->d, at->n_q_heads / pg->H);
+  return attn_workspace_bytes(pg);
 }
 
 kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, const void* q,
@@ -277,8 +290,8 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
   KVC_TRY(check_paged(pg));
   KVC_TRY(check_head_dim(pg));
   KVC_TRY(check_attn(pg, at));
-  KVC_TRY(check_view(pg, pool_K, "pool_K"));
-  KVC_TRY(check_view(pg, pool_V, "pool_V"));
+  KVC_TRY(check_pool(pg, pool_K, "pool_K"));
+  KVC_TRY(check_pool(pg, pool_V, "pool_V"));
   if (at->n_tokens > 0) {
     if (pg->R > 0) {
       KVC_TRY(check_ptr(block_table, "block_table", 4));
@@ -287,13 +300,11 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
     }
     KVC_TRY(check_rows(pg, at, q, at->q_s_tok, at->q_s_head, "q"));
     KVC_TRY(check_rows(pg, at, out, at->out_s_tok, at->out_s_head, "out"));
-    if (at->out_s_tok < pg->d && at->n_tokens > 1)
-      return fail(KVC_ERR_SHAPE, "out: the token stride must be >= d");
   }
   if (reinterpret_cast<uintptr_t>(lse) & 3)
     return fail(KVC_ERR_ALIGNMENT, "lse must be 4-byte aligned");
   KVC_TRY(check_ptr(dev_status, "dev_status", 4));
-  const size_t bytes = attn_workspace_bytes(pg->dtype, pg->d, at->n_q_heads / pg->H);
+  const size_t bytes = attn_workspace_bytes(pg);
   if (workspace == nullptr || workspace_bytes < bytes)
     return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", bytes,
                 workspace == nullptr ? size_t(0) : workspace_bytes);
@@ -343,7 +354,8 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
   a.scale_log2 = at->scale * 1.4426950408889634f;
   a.workspace = workspace;
   a.dev_status = dev_status;
-  const cudaError_t e = launch_attn_simt(a, pg->dtype, stream);
+  const cudaError_t e =
+      pg->dtype == KVC_BF16 ? launch_attn_tc(a, stream) : launch_attn_simt(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvc_paged_attention launch");
   return KVC_OK;
 }
