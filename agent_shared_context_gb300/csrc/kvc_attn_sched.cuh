@@ -21,6 +21,25 @@
 namespace kvc {
 namespace attn {
 
+// Division by a divisor that a call fixes (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): exact for 0 <= n < 2^31.
+struct FastDiv {
+  uint32_t mul, shift;
+  int32_t d;
+};
+
+inline FastDiv make_fastdiv(int32_t d) {
+  FastDiv f{0, 0, d};
+  while ((int64_t(1) << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - d)) / d + 1);
+  return f;
+}
+
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  const uint32_t u = static_cast<uint32_t>(n);
+  return static_cast<int>((__umulhi(u, f.mul) + u) >> f.shift);
+}
+
 // Everything a kernel needs to divide the work (by value, all host-checked).
 struct SchedArgs {
   const int32_t* q_start;   // [R + 1]
@@ -28,10 +47,11 @@ struct SchedArgs {
   int32_t R, H, N;          // requests, KV heads, query tokens
   int32_t kv_cap;           // max_blocks * page_size
   int32_t causal, window;
-  int32_t tok_item;         // query tokens per item
-  int32_t group_tok;        // key tokens of a tile group (a page or several, below)
+  FastDiv item;             // query tokens per item
+  FastDiv group;            // key tokens of a tile group (a page or several, below)
+  FastDiv tile;             // key tokens per tile inside a group
   int32_t group_tiles;      // tiles per group
-  int32_t tile_tok;         // key tokens per tile inside a group
+  int32_t even;             // tile t holds the tokens [t tile, (t + 1) tile)
 };
 
 struct Request {
@@ -40,24 +60,21 @@ struct Request {
 
 // Table values come from the device: whatever they hold, rows stay in [0, N)
 // and keys in [0, kv_cap].
-__device__ __forceinline__ Request load_request(const SchedArgs& a, int r) {
+__device__ __forceinline__ Request load_request(const SchedArgs& a, int r, bool* bad = nullptr) {
   Request q;
-  const int s0 = a.q_start[r], s1 = a.q_start[r + 1];
+  const int s0 = __ldg(a.q_start + r), s1 = __ldg(a.q_start + r + 1), n = __ldg(a.kv_lens + r);
   q.q0 = min(max(s0, 0), a.N);
   q.nq = min(max(s1, q.q0), a.N) - q.q0;
-  q.kv = min(max(a.kv_lens[r], 0), a.kv_cap);
+  q.kv = min(max(n, 0), a.kv_cap);
   q.pos0 = q.kv - q.nq;
+  if (bad != nullptr) *bad |= s0 < 0 || s1 < s0 || s1 > a.N || n < 0 || n > a.kv_cap;
   return q;
 }
 
-__device__ __forceinline__ bool request_out_of_range(const SchedArgs& a, int r) {
-  const int s0 = a.q_start[r], s1 = a.q_start[r + 1], n = a.kv_lens[r];
-  return s0 < 0 || s1 < s0 || s1 > a.N || n < 0 || n > a.kv_cap;
-}
-
 __device__ __forceinline__ int tile_of(const SchedArgs& a, int tok) {
-  const int g = tok / a.group_tok;
-  return g * a.group_tiles + (tok - g * a.group_tok) / a.tile_tok;
+  if (a.even) return fast_div(tok, a.tile);
+  const int g = fast_div(tok, a.group);
+  return g * a.group_tiles + fast_div(tok - g * a.group.d, a.tile);
 }
 
 // Key tiles [lo, hi) that query tokens [t0, t1) of the request can see.  An
@@ -75,19 +92,53 @@ __device__ __forceinline__ void item_tiles(const SchedArgs& a, const Request& q,
   *hi = tile_of(a, k1 - 1) + 1;
 }
 
-__device__ __forceinline__ int n_items(const SchedArgs& a, const Request& q) {
-  return (q.nq + a.tok_item - 1) / a.tok_item;
+__device__ __forceinline__ int item_units(const SchedArgs& a, const Request& q, int i) {
+  int lo, hi;
+  item_tiles(a, q, i * a.item.d, min(q.nq, (i + 1) * a.item.d), &lo, &hi);
+  return hi - lo;
 }
 
-// Units of one KV head of a request.
-__device__ __forceinline__ int64_t head_units(const SchedArgs& a, const Request& q) {
-  int64_t u = 0;
-  const int n = n_items(a, q);
-  for (int i = 0; i < n; ++i) {
-    int lo, hi;
-    item_tiles(a, q, i * a.tok_item, min(q.nq, (i + 1) * a.tok_item), &lo, &hi);
-    u += hi - lo;
+__device__ __forceinline__ int n_items(const SchedArgs& a, const Request& q) {
+  return fast_div(q.nq + a.item.d - 1, a.item);
+}
+
+// sum over 0 <= i < n of floor((a i + b) / m), by the steps of Euclid's
+// algorithm on (a, m).
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += static_cast<int64_t>(n) * (b / m);
+      b %= m;
+    }
+    const uint32_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y - n * m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
   }
+  return s;
+}
+
+// Units of the request's first `n` items of one KV head.  A plain causal chunk
+// (every chunk without a window, on pages that fill their tiles) has a closed
+// form: item i sees ceil((pos0 + (i + 1) item) / tile) tiles.
+__device__ __forceinline__ int64_t first_units(const SchedArgs& a, const Request& q, int n) {
+  if (n <= 0) return 0;
+  if (a.even && a.window == 0 && n > 2) {
+    const int64_t last = item_units(a, q, n - 1);      // the last may be shorter than an item
+    if (!a.causal) return last * n;
+    if (q.pos0 >= 0)
+      return last + floor_sum(n - 1, a.tile.d, a.item.d, q.pos0 + a.item.d + a.tile.d - 1);
+  }
+  int64_t u = 0;
+  for (int i = 0; i < n; ++i) u += item_units(a, q, i);
   return u;
 }
 
@@ -101,14 +152,23 @@ struct Item {
 
 struct Shared {
   int64_t warp_sum[32];
-  int64_t total;
-  int64_t begin_off;   // units of the start request before the share's first unit
-  int32_t begin_r;
+  int64_t off;         // units before the share's first in what is searched
+  int32_t r, h, i;     // where the share begins
+  int32_t item_off;    // units of that item before the share
 };
 
 // CTA that owns unit u when U units are cut into n shares [c U / n, (c+1) U / n).
 __device__ __forceinline__ int owner_of(int64_t u, int64_t U, int n) {
-  return static_cast<int>(((u + 1) * n - 1) / U);
+  const int64_t x = (u + 1) * n - 1;
+  if (x < (int64_t(1) << 32) && U < (int64_t(1) << 32))
+    return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(U));
+  return static_cast<int>(x / U);
+}
+
+__device__ __forceinline__ int64_t share_start(int c, int64_t U, int n) {
+  const int64_t x = c * U;
+  if (x < (int64_t(1) << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(n);
+  return x / n;
 }
 
 // Walks the share of one CTA.  All threads that walk hold the same state.
@@ -125,7 +185,7 @@ struct Walker {
     if (u >= u1) return false;
     for (;;) {
       if (i < n) {
-        const int t0 = i * a.tok_item, t1 = min(q.nq, t0 + a.tok_item);
+        const int t0 = i * a.item.d, t1 = min(q.nq, t0 + a.item.d);
         int lo, hi;
         item_tiles(a, q, t0, t1, &lo, &hi);
         const int64_t end = item_u0 + (hi - lo);
@@ -196,8 +256,8 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
     const int r = base + tid;
     mine = 0;
     if (r < a.R) {
-      bad |= request_out_of_range(a, r);
-      mine = head_units(a, load_request(a, r)) * a.H;
+      const Request q = load_request(a, r, &bad);
+      mine = first_units(a, q, n_items(a, q)) * a.H;
     }
     int64_t total;
     incl = block_inclusive<THREADS>(mine, sh, &total);
@@ -206,46 +266,60 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
   if (bad && blockIdx.x == 0) atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
   // no empty shares between others: an item's parts are consecutive CTAs
   const int n = static_cast<int>(U < gridDim.x ? U : gridDim.x);
-  const bool idle = static_cast<int>(blockIdx.x) >= n;
-  const int64_t u0 = idle ? U : U * blockIdx.x / n;
-  if (tid == 0) {
-    sh->begin_r = a.R;
-    sh->begin_off = 0;
-  }
-  __syncthreads();
+  Walker w;
+  w.U = U;
+  w.grid = n;
+  w.u = w.u1 = w.item_u0 = U;
+  w.r = a.R;
+  w.h = w.i = w.n = 0;
+  w.q = Request{0, 0, 0, 0};
+  if (static_cast<int>(blockIdx.x) >= n) return w;
+  w.u = share_start(blockIdx.x, U, n);
+  w.u1 = share_start(blockIdx.x + 1, U, n);
+  // the request of unit u ...
   int64_t before = 0;
   for (int base = 0; base < a.R; base += THREADS) {
     const int r = base + tid;
     int64_t total = U;
     if (a.R > THREADS) {             // one chunk: the first pass's sums still stand
-      mine = r < a.R ? head_units(a, load_request(a, r)) * a.H : 0;
+      mine = 0;
+      if (r < a.R) {
+        const Request q = load_request(a, r);
+        mine = first_units(a, q, n_items(a, q)) * a.H;
+      }
       incl = block_inclusive<THREADS>(mine, sh, &total);
     }
-    if (before + incl > u0 && before + incl - mine <= u0) {   // one thread at most
-      sh->begin_r = r;
-      sh->begin_off = u0 - (before + incl - mine);
+    if (before + incl > w.u && before + incl - mine <= w.u) {   // one thread
+      const int64_t off = w.u - (before + incl - mine);
+      const int64_t hu = mine / a.H;
+      sh->r = r;
+      sh->h = static_cast<int>(off / hu);
+      sh->off = off - sh->h * hu;
     }
     before += total;
-    if (before > u0) break;
+    if (before > w.u) break;
   }
   __syncthreads();
-  Walker w;
-  w.U = U;
-  w.u = u0;
-  w.u1 = idle ? U : U * (blockIdx.x + 1) / n;
-  w.grid = n;
-  w.r = sh->begin_r;
-  w.h = 0;
-  w.i = 0;
-  w.n = 0;
-  w.item_u0 = u0;
-  w.q = Request{0, 0, 0, 0};
-  if (w.u < w.u1) {
-    w.q = load_request(a, w.r);
-    w.n = n_items(a, w.q);
-    const int64_t hu = head_units(a, w.q);
-    w.h = static_cast<int>(sh->begin_off / hu);
-    w.item_u0 = u0 - (sh->begin_off - w.h * hu);
+  w.r = sh->r;
+  w.h = sh->h;
+  w.q = load_request(a, w.r);
+  w.n = n_items(a, w.q);
+  // ... and its item
+  const int64_t off = sh->off;
+  if (w.n == 1) {
+    w.item_u0 = w.u - off;
+  } else {
+    for (int i = tid; i < w.n; i += THREADS) {
+      const int64_t p = first_units(a, w.q, i);
+      if (p <= off && off < p + item_units(a, w.q, i)) {        // one thread
+        sh->i = i;
+        sh->item_off = static_cast<int>(off - p);
+      }
+      if (p > off) break;
+    }
+    __syncthreads();
+    w.i = sh->i;
+    w.item_u0 = w.u - sh->item_off;
   }
   return w;
 }
@@ -254,8 +328,10 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
 // A share leaves at most two parts of divided items: the end of an item that
 // an earlier share began (slot 0) and the beginning of one that a later share
 // goes on with (slot 1); an item that covers the whole share takes slot 0.
-// A slot holds O [rows][d], m [rows] and l [rows] in fp32 with m in units of
-// log2: the rows' softmax is sum exp2(x - m) = l and O = sum exp2(x - m) v.
+// A slot holds O, m and l of its rows in fp32, with m in units of log2: the
+// row's softmax is sum exp2(x - m) = l and O = sum exp2(x - m) v.  O lies as
+// [d / 4][rows] groups of four columns, so that threads that each have a row
+// write and read neighbouring 16 bytes.
 __host__ __device__ inline size_t slot_floats(int rows, int d) {
   return static_cast<size_t>(rows) * (d + 2);
 }
@@ -265,6 +341,69 @@ __device__ __forceinline__ int slot_of(int part) { return part == 0 ? 1 : 0; }
 // exp2(m - M) for a part's weight, 0 for a part that saw nothing.
 __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return l == 0.0f ? 0.0f : exp2f(m - M);
+}
+
+// One of `n_threads` threads joins the parts of rows [0, rows) of an item and
+// hands (row, first column, four values of O / l, lse in nats) to `store`.
+// Part p lies in slot slot_of(p) of CTA cta0 + p, `slot_rows` rows with row0
+// the first.  Parts are added in the order of their keys.
+template <typename Store>
+__device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, int slot_rows,
+                                           int row0, int d, const Item& it, int rows, int tid,
+                                           int n_threads, Store store) {
+  // threads over rows first, then over groups of columns; a thread keeps its row
+  int span = 1;
+  while (span < rows) span <<= 1;
+  if (span > n_threads) span = n_threads;
+  const int d4 = d / 4, step = n_threads / span;
+  const float* base = slots + static_cast<size_t>(it.cta0) * 2 * slot_n;
+  for (int row = tid & (span - 1); row < rows; row += span) {
+    auto part = [&](int p) { return base + (static_cast<size_t>(p) * 2 + slot_of(p)) * slot_n; };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int p = 0; p < it.nparts; ++p)
+      M = fmaxf(M, __ldcg(part(p) + slot_rows * d + row0 + row));
+    constexpr int kC = 8;
+    for (int c0 = tid / span; c0 < d4; c0 += kC * step) {
+      float4 acc[kC];
+      float L = 0.f;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int p = 0; p < it.nparts; ++p) {
+        const float* ps = part(p);
+        const float m = __ldcg(ps + slot_rows * d + row0 + row);
+        const float l = __ldcg(ps + slot_rows * d + slot_rows + row0 + row);
+        float4 v[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (c0 + c * step < d4)
+            v[c] = __ldcg(reinterpret_cast<const float4*>(ps) + (c0 + c * step) * slot_rows +
+                          row0 + row);
+        if (l == 0.f) continue;
+        const float f = part_weight(m, l, M);
+        L = fmaf(l, f, L);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (c0 + c * step < d4) {
+            acc[c].x = fmaf(v[c].x, f, acc[c].x);
+            acc[c].y = fmaf(v[c].y, f, acc[c].y);
+            acc[c].z = fmaf(v[c].z, f, acc[c].z);
+            acc[c].w = fmaf(v[c].w, f, acc[c].w);
+          }
+      }
+      const float inv = 1.f / L;
+      const float lse = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        if (c0 + c * step < d4)
+          store(row, (c0 + c * step) * 4,
+                L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                         : make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv,
+                                       acc[c].w * inv),
+                lse);
+    }
+  }
 }
 
 }  // namespace attn

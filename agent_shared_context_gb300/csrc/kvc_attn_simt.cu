@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
         const int col = tx * 4 + c * 64;
-        if (col < d) store4(slot + row * d + col, o[i][c]);
+        if (col < d) store4(slot + (col / 4 * kSlotRows + row) * 4, o[i][c]);
       }
       if (tx == 0) {
         slot[kSlotRows * d + row] = m[i];
@@ -237,36 +237,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
     if (!sh.last) continue;
     __threadfence();
     if (tid == 0) counters[it.cta0] = 0;
-    for (int i = tid; i < rows * dv; i += kThreads) {
-      const int row = i / dv, col = (i - row * dv) * 4;
-      float M = -INFINITY;
-      for (int p = 0; p < it.nparts; ++p) {
-        const float* ps = slots + (static_cast<size_t>(it.cta0 + p) * 2 + slot_of(p)) * slot_n;
-        M = fmaxf(M, __ldcg(ps + kSlotRows * d + row));
-      }
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p = 0; p < it.nparts; ++p) {
-        const float* ps = slots + (static_cast<size_t>(it.cta0 + p) * 2 + slot_of(p)) * slot_n;
-        const float pm = __ldcg(ps + kSlotRows * d + row);
-        const float pl = __ldcg(ps + kSlotRows * d + kSlotRows + row);
-        if (pl == 0.f) continue;
-        const float f = part_weight(pm, pl, M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + row * d + col));
-        L = fmaf(pl, f, L);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
-      store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
-             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (a.lse != nullptr && col == 0)
-        a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    }
+    join_parts(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
+               [&](int row, int col, float4 v, float lse) {
+                 const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
+                 store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
+                        v);
+                 if (a.lse != nullptr && col == 0)
+                   a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] = lse;
+               });
   }
 }
 
@@ -291,10 +269,10 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   s.kv_cap = a.width * a.B;
   s.causal = a.causal;
   s.window = a.window;
-  s.tok_item = rows / a.G;
-  s.group_tok = kTile;
+  s.item = make_fastdiv(rows / a.G);
+  s.group = s.tile = make_fastdiv(kTile);
   s.group_tiles = 1;
-  s.tile_tok = kTile;
+  s.even = 1;
   const int per_sm = smem * 2 + 4096 <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
   const int grid = di.sm_count * per_sm < kMaxCtas ? di.sm_count * per_sm : kMaxCtas;
   fn<<<grid, kThreads, smem, stream>>>(a, s);

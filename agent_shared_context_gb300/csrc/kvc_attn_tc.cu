@@ -26,8 +26,9 @@
 //   warp 8          walks the share, hands the items to the others through a
 //                   ring, looks the pages up and issues the TMA loads of Q, K
 //                   and V;
-//   warp 9          issues S = Q K^T (both K-major in shared memory) and
-//                   O += P V (P in TMEM, V as the MN-major operand it is);
+//   warps 9, 11     issue stream 0's and 1's S = Q K^T (both K-major in shared
+//                   memory) and O += P V (P in TMEM, V as the MN-major operand
+//                   it is);
 //   warp 10         mends value tiles at the edge of sight (below).
 //
 // A key tile is 128 rows of a page, or as many whole pages (rounded up to 8
@@ -41,9 +42,9 @@
 // The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
 // 2^-8 average out over many keys of like weight but not where few carry a
 // row, so the remainder P - bf16(P) is multiplied too, in the steps of 16 keys
-// in which some row has a key with more than 1/8 of its sum so far (pair mode)
-// or in all (single mode, which waits for memory anyway): few steps of a long
-// context.  S leaves room for it in TMEM, beside P.
+// in which some row has a key with more than 1/8 of its sum so far (1/16 in
+// single mode, which waits for memory anyway): few steps of a long context.  S
+// leaves room for it in TMEM, beside P.
 //
 // Every wait is bounded: one that expires stores KVC_ERR_DEVICE_TIMEOUT into
 // *dev_status and raises the CTA's abort flag; the roles stop, copies and MMAs
@@ -62,7 +63,7 @@ namespace {
 using namespace ptx;
 using namespace attn;
 
-constexpr int kThreads = 384;              // 12 warps (roles above, the last one idle)
+constexpr int kThreads = 384;              // 12 warps (roles above)
 constexpr int kRegsSoftmax = 208;          // 256 threads x 208 + 128 x 88 = 384 x 168, the launch's
 constexpr int kRegsOther = 88;
 constexpr int kRowsM = 128;                // rows of a stream (MMA M)
@@ -71,8 +72,10 @@ constexpr int kSubBytes = kTile * 128;     // 128 rows x 64 bf16
 constexpr int kSlotRows = 256;             // rows of a partial result
 constexpr int kMaxCtas = 160;
 constexpr int kItems = 4;                  // depth of the item ring
+constexpr int kNoPage = INT32_MIN;         // no key there: read as zeros
 constexpr float kLag = 8.0f;               // log2 by which m may lag behind
-constexpr float kHeavy = 0.125f;           // share of a row's sum that makes a key heavy
+constexpr float kHeavyPair = 0.125f;       // share of a row's sum that makes a key heavy
+constexpr float kHeavySingle = 0.0625f;
 
 template <int D>
 struct Cfg {
@@ -90,16 +93,25 @@ struct TcMaps {
 struct TcArgs {
   AttnArgs a;
   SchedArgs s;
+  FastDiv page, rows, tiles;   // by B, by page_rows, by the tiles of a group
   int32_t tok_tile;        // tokens of a row tile, floor(128 / G)
   int32_t page_rows;       // rows of a page in a tile: B rounded up to 8, or 128
   int32_t pages_tile;      // pages of a tile (1 if a page has 128 rows or more)
   uint32_t holes[4];       // columns of a tile that never hold a key (pages < 128 rows)
   int32_t has_holes;
+  int32_t ragged;          // some tiles hold fewer than 128 keys
 };
 
 struct ItemSlot {
   Item it;
   int32_t ring0;           // ring position of the item's first K tile
+  int32_t edge_lo, edge_hi;  // key tiles below and from which value rows need mending
+};
+
+// What a stream's softmax tells its MMA warp along with P.
+struct alignas(8) Told {
+  uint32_t heavy;          // steps of 16 keys with a remainder, a byte per warp
+  int32_t o_init;          // O holds something before the first P V
 };
 
 template <int NS>
@@ -107,15 +119,16 @@ struct Bars {
   uint64_t kv_full[NS], kv_raw[NS], kv_empty[NS];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2];
+  uint64_t o_seen[2];              // the stream's warps know that an item's O is complete
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t ml_full, ml_empty;      // stream 1's row statistics for stream 0
   uint64_t wg[2];                  // the four warps of a stream
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t last[2];
-  int32_t o_init[2];               // O holds something before the first P V
-  uint32_t heavy[2];               // steps of 16 keys with a remainder, a byte per warp
+  Told told[2];
+  int32_t mended[2];               // value tiles of each stream that were mended so far
   uint32_t poison[NS][4];          // cleared value rows that some rows of the item see
   float ml[kRowsM][2];
   ItemSlot items[kItems];
@@ -125,7 +138,7 @@ struct Bars {
 template <int NS>
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Bars<NS>* b,
                                               int32_t* dev_status) {
-  if (mbar_wait_bounded(bar, parity, kWaitLimitNs, &b->abort_flag)) return true;
+  if (mbar_wait_polling(bar, parity, kWaitLimitNs, &b->abort_flag)) return true;
   volatile int32_t* ab = &b->abort_flag;
   if (*ab == 0) {
     *ab = 1;
@@ -134,7 +147,31 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Ba
   return false;
 }
 
-// The same for a whole warp: all lanes give up together.
+// Waits until *count, which another warp raises, has reached `want`.
+template <int NS>
+__device__ __forceinline__ bool warp_wait_count(const int32_t* count, int32_t want, Bars<NS>* b,
+                                                int32_t* dev_status) {
+  const volatile int32_t* c = count;
+  volatile int32_t* ab = &b->abort_flag;
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (uint32_t i = 1; *c - want < 0; ++i) {
+    if ((i & 4095u) != 0u) continue;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (*ab == 0 && t - t0 <= kWaitLimitNs) continue;
+    if (*ab == 0) {
+      *ab = 1;
+      atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_DEVICE_TIMEOUT));
+    }
+    ok = false;
+    break;
+  }
+  __threadfence_block();
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A bounded wait of a whole warp: all lanes give up together.
 template <int NS>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b,
                                           int32_t* dev_status) {
@@ -169,9 +206,14 @@ struct TileSpan {
 
 __device__ __forceinline__ TileSpan tile_span(const TcArgs& p, int tile) {
   TileSpan t;
-  const int g = tile / p.s.group_tiles, sub = tile - g * p.s.group_tiles;
-  t.tok0 = g * p.s.group_tok + sub * p.s.tile_tok;
-  t.cnt = min(p.s.tile_tok, p.s.group_tok - sub * p.s.tile_tok);
+  if (p.s.even) {
+    t.tok0 = tile * p.s.tile.d;
+    t.cnt = p.s.tile.d;
+  } else {
+    const int g = fast_div(tile, p.tiles), sub = tile - g * p.s.group_tiles;
+    t.tok0 = g * p.s.group.d + sub * p.s.tile.d;
+    t.cnt = min(p.s.tile.d, p.s.group.d - sub * p.s.tile.d);
+  }
   return t;
 }
 
@@ -181,15 +223,15 @@ __device__ __forceinline__ int tile_col(const TcArgs& p, const TileSpan& t, int 
   const int rel = tok - t.tok0;
   if (rel <= 0) return 0;
   if (rel >= t.cnt) return kTile;
-  if (p.pages_tile == 1) return rel;
-  const int pg = rel / p.a.B;
+  if (!p.has_holes) return rel;
+  const int pg = fast_div(rel, p.page);
   return pg * p.page_rows + (rel - pg * p.a.B);
 }
 
 // Token of a key column (not of a hole).
 __device__ __forceinline__ int tile_tok(const TcArgs& p, const TileSpan& t, int col) {
-  if (p.pages_tile == 1) return t.tok0 + col;
-  const int pg = col / p.page_rows;
+  if (!p.has_holes) return t.tok0 + col;
+  const int pg = fast_div(col, p.rows);
   return t.tok0 + pg * p.a.B + (col - pg * p.page_rows);
 }
 
@@ -207,9 +249,11 @@ __device__ __forceinline__ Sight sight(const AttnArgs& a, int kv, int pos0, int 
   return s;
 }
 
-// Whether the tile's value rows need mending before the product.
-__device__ __forceinline__ bool at_edge(const TileSpan& t, const Sight& s) {
-  return t.tok0 + t.cnt > s.all_hi || t.tok0 < s.all_lo;
+// Key tiles that not every row sees whole: below *lo and from *hi on.  Their
+// value rows are mended before the product.
+__device__ __forceinline__ void edges(const SchedArgs& a, const Sight& s, int* lo, int* hi) {
+  *lo = s.all_lo > 0 ? tile_of(a, s.all_lo - 1) + 1 : 0;
+  *hi = s.all_hi > 0 ? tile_of(a, s.all_hi) : 0;
 }
 
 __device__ __forceinline__ uint32_t bits_below(int n) {      // n lowest bits
@@ -237,23 +281,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&b->kv_full[i], 1);
       mbar_init(&b->kv_raw[i], 1);
-      mbar_init(&b->kv_empty[i], 1);
+      mbar_init(&b->kv_empty[i], 2);       // one MMA warp for each stream
     }
     mbar_init(&b->q_full, 1);
-    mbar_init(&b->q_empty, 1);
+    mbar_init(&b->q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b->s_full[i], 1);
       mbar_init(&b->p_full[i], 4);
+      mbar_init(&b->o_seen[i], 4);
       mbar_init(&b->wg[i], 4);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&b->item_full[i], 1);
-      mbar_init(&b->item_empty[i], 10);    // 8 softmax warps, the MMA and the mending warp
+      mbar_init(&b->item_empty[i], 11);    // 8 softmax, 2 MMA warps and the mending one
     }
     mbar_init(&b->ml_full, 4);
     mbar_init(&b->ml_empty, 4);
-    mbar_init(&b->drain, 1);
+    mbar_init(&b->drain[0], 1);
+    mbar_init(&b->drain[1], 1);
     b->abort_flag = 0;
+    b->mended[0] = b->mended[1] = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -280,16 +327,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
 
+  if (warp >= 8) {
+  regs_lower<kRegsOther>();                       // one instruction for the whole warpgroup
   if (warp == 8) {
     // ------------------------------------------------------------ producer
-    regs_lower<kRegsOther>();
     int ring = 0, n_items = 0;
+    int s = 0;                                    // ring % NS
+    uint32_t wrap = 1;                            // parity of kv_empty[s] to wait for
     bool ok = true;
     uint32_t raw_phase = 0;                       // bit i: parity of kv_raw[i]'s next phase
     uint32_t raw_open = 0;                        // bit i: slot i's last load went to kv_raw
     const int boxes = p.pages_tile * C::kSub;
     const int my_page = lane / C::kSub, my_sub = lane - my_page * C::kSub;
     const uint32_t tile_bytes = static_cast<uint32_t>(p.pages_tile * p.page_rows) * 128 * C::kSub;
+    uint8_t* my_dst = kv_smem + my_sub * kSubBytes + my_page * p.page_rows * 128;
     bool bad_page = false;
 
     for (;;) {
@@ -299,15 +350,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&b->item_empty[slot], ((n_items / kItems) & 1) ^ 1, b, a.dev_status);
       if (!ok) break;
       if (!more) it.ntiles = 0;
+      int edge_lo = 0, edge_hi = 0;
+      if (more) edges(p.s, sight(a, it.kv, it.pos0, it.nt), &edge_lo, &edge_hi);
       if (lane == 0) {
         b->items[slot].it = it;
         b->items[slot].ring0 = ring;
+        b->items[slot].edge_lo = edge_lo;
+        b->items[slot].edge_hi = edge_hi;
         mbar_arrive(&b->item_full[slot]);
       }
       __syncwarp();
       if (!more) break;
       const bool pair = it.nt > p.tok_tile;
-      const Sight see = sight(a, it.kv, it.pos0, it.nt);
+
+      // The pages of the lane's boxes of key tiles 0, 1, ... in order (`blk`,
+      // `sub`: page and tile in it).  A box beyond the pool (page P) is filled with 0.
+      const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
+      const int last_blk = it.kv > 0 ? fast_div(it.kv - 1, p.page) : -1;
+      int blk, sub = 0;
+      if (p.pages_tile == 1) {
+        blk = fast_div(it.tile0, p.tiles);
+        sub = it.tile0 - blk * p.s.group_tiles;
+      } else {
+        blk = it.tile0 * p.pages_tile + my_page;
+      }
+      auto next_page = [&]() -> int {              // unchecked: looked at when it is used
+        const int page = lane < boxes && blk <= last_blk ? __ldg(table + blk) : kNoPage;
+        if (p.pages_tile > 1) {
+          blk += p.pages_tile;
+        } else if (++sub == p.s.group_tiles) {
+          sub = 0;
+          ++blk;
+        }
+        return page;
+      };
+      int pg0 = next_page(), pg1 = next_page();
 
       // Q: one box per row tile and 64 columns
       ok = warp_wait(&b->q_empty, (n_items & 1) ^ 1, b, a.dev_status);
@@ -323,48 +400,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++n_items;
 
-      auto load = [&](int kv, int i) -> bool {
-        const int s = ring % NS;
-        if (!warp_wait(&b->kv_empty[s], ((ring / NS) & 1) ^ 1, b, a.dev_status)) return false;
-        const int tile = it.tile0 + i;
-        const int g = tile / p.s.group_tiles;
-        uint64_t* bar = &b->kv_full[s];
-        raw_open &= ~(1u << s);
-        if (kv == 1 && at_edge(tile_span(p, tile), see)) {
-          bar = &b->kv_raw[s];
-          raw_open |= 1u << s;
-          raw_phase ^= 1u << s;
+      int row_k = 0, row_v = 0;                    // first row of the tile in its page
+      if (p.pages_tile == 1)
+        row_k = row_v = (it.tile0 - fast_div(it.tile0, p.tiles) * p.s.group_tiles) * kTile;
+      const int row_end = p.pages_tile == 1 ? p.s.group_tiles * kTile : kTile;
+      auto load = [&](const CUtensorMap* map, int page, int& row, bool mend) -> bool {
+        uint64_t* bar = mend ? &b->kv_raw[s] : &b->kv_full[s];
+        if (!warp_wait(&b->kv_empty[s], wrap, b, a.dev_status)) return false;
+        if (page < 0 || page >= a.P) {
+          bad_page |= page != kNoPage;
+          page = a.P;
         }
         if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
         __syncwarp();
-        if (lane < boxes) {
-          const int blk = p.pages_tile == 1 ? g : g * p.pages_tile + my_page;
-          const int row = p.pages_tile == 1 ? (tile - g * p.s.group_tiles) * kTile : 0;
-          int page = a.P;                          // beyond the pool: the box is filled with 0
-          if (static_cast<int64_t>(blk) * a.B < it.kv) {
-            page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
-            if (page < 0 || page >= a.P) {
-              page = a.P;
-              bad_page = true;
-            }
-          }
-          tma_load_5d(kv_smem + s * C::kSlotBytes + my_sub * kSubBytes +
-                          my_page * p.page_rows * 128,
-                      kv == 0 ? &maps.k : &maps.v, bar, my_sub * 64, row, it.h, a.layer, page);
-        }
-        __syncwarp();
+        if (lane < boxes)
+          tma_load_5d(my_dst + s * C::kSlotBytes, map, bar, my_sub * 64, row, it.h, a.layer, page);
+        row += kTile;
+        if (row == row_end) row = 0;
+        raw_open = mend ? raw_open | 1u << s : raw_open & ~(1u << s);
+        raw_phase ^= static_cast<uint32_t>(mend) << s;
         ++ring;
+        if (++s == NS) {
+          s = 0;
+          wrap ^= 1;
+        }
         return true;
       };
       const int n = it.ntiles;
+      auto load_k = [&](int page) { return load(&maps.k, page, row_k, false); };
+      auto load_v = [&](int page, int i) {
+        const int tile = it.tile0 + i;
+        return load(&maps.v, page, row_v, tile < edge_lo || tile >= edge_hi);
+      };
       if (pair) {
-        for (int i = 0; i < n && ok; ++i) ok = load(0, i) && load(1, i);
-      } else {
-        ok = load(0, 0);
-        if (ok && n > 1) ok = load(0, 1);
         for (int i = 0; i < n && ok; ++i) {
-          ok = load(1, i);
-          if (ok && i + 2 < n) ok = load(0, i + 2);
+          const int pg2 = next_page();
+          ok = load_k(pg0) && load_v(pg0, i);
+          pg0 = pg1;
+          pg1 = pg2;
+        }
+      } else {
+        ok = load_k(pg0) && (n == 1 || load_k(pg1));
+        for (int i = 0; i < n && ok; ++i) {
+          const int pg2 = next_page();
+          ok = load_v(pg0, i) && (i + 2 >= n || load_k(pg2));
+          pg0 = pg1;
+          pg1 = pg2;
         }
       }
       if (!ok) break;
@@ -381,127 +462,126 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n_items > 0) mbar_wait_bounded(&b->q_full, (n_items - 1) & 1, kWaitLimitNs);
     }
-  } else if (warp == 9) {
-    // ----------------------------------------------------------------- MMA
-    regs_lower<kRegsOther>();
-    if (lane == 0) {
-      uint32_t ph_p[2] = {0, 0};
-      bool ok = true;
-      for (int n_items = 0; ok; ++n_items) {
-        const int slot = n_items % kItems;
-        ok = wait_or_abort(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
-        if (!ok) break;
-        const int n = b->items[slot].it.ntiles;
-        if (n == 0) break;
-        const bool pair = b->items[slot].it.nt > p.tok_tile;
-        const int ring0 = b->items[slot].ring0;
-        mbar_arrive(&b->item_empty[slot]);
+  } else if (warp == 9 || warp == 11) {
+    // ------------------------------------------------- MMAs of one stream
+    // Values that every MMA needs come from lane 0, so that they are uniform to
+    // the compiler too and stay in uniform registers.
+    const int st = __shfl_sync(0xffffffffu, warp == 9 ? 0 : 1, 0);
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t dS = base + st * 128, dO = base + 256 + st * D;
+    // low words of the shared-memory descriptors
+    const uint64_t desc_q = desc_kmajor_sw128(smem_u32(q_smem));
+    const uint64_t desc_k = desc_kmajor_sw128(smem_u32(kv_smem));
+    const uint64_t desc_v = desc_mnmajor_sw128(smem_u32(kv_smem), kSubBytes);
+    uint32_t ph_p = 0, ph_o = 0;
+    bool ended = false;                            // an item's O may not be seen yet
+    bool ok = true;
+    for (int n_items = 0; ok; ++n_items) {
+      const int slot = n_items % kItems;
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      if (!ok) break;
+      const int n = __shfl_sync(0xffffffffu, b->items[slot].it.ntiles, 0);
+      if (n == 0) break;
+      const bool pair = __shfl_sync(0xffffffffu, b->items[slot].it.nt, 0) > p.tok_tile;
+      const int ring0 = __shfl_sync(0xffffffffu, b->items[slot].ring0, 0);
+      if (lane == 0) mbar_arrive(&b->item_empty[slot]);
+      __syncwarp();
+      const int first = pair ? 0 : st, step = pair ? 1 : 2;
+      const uint64_t dq = desc_q + static_cast<uint64_t>((pair ? st : 0) * (C::kSlotBytes >> 4));
 
-        auto full = [&](int pos) {
-          return wait_or_abort(&b->kv_full[pos % NS], (pos / NS) & 1, b, a.dev_status);
-        };
-        auto qk = [&](int st, int pos) {
-          const uint32_t qa = smem_u32(q_smem + (pair ? st : 0) * C::kSlotBytes);
-          const uint32_t ka = smem_u32(kv_smem + (pos % NS) * C::kSlotBytes);
+      // Both MMA warps see every tile of the ring pass, in its order, and both free
+      // every slot: a wait on a parity is only good for the next phase.
+      auto full = [&](int pos) {
+        return warp_wait(&b->kv_full[pos % NS], (pos / NS) & 1, b, a.dev_status);
+      };
+      int seen = ring0;                            // single mode: next position not seen
+      auto pass_to = [&](int pos) {                // tiles of the other stream
+        for (; seen < pos; ++seen) {
+          if (!full(seen)) return false;
+          if (lane == 0) mbar_arrive(&b->kv_empty[seen % NS]);
+          __syncwarp();
+        }
+        return true;
+      };
+      auto own = [&](int pos) {
+        if (!pair && !pass_to(pos)) return false;
+        seen = pos + 1;
+        return full(pos);
+      };
+      auto done = [&](int pos) { mma_commit_warp(&b->kv_empty[pos % NS]); };
+      ok = warp_wait(&b->q_full, n_items & 1, b, a.dev_status);
+      if (!ok) break;
+      if (first >= n) {                            // single mode, one tile: none for stream 1
+        if (lane == 0) mbar_arrive(&b->q_empty);
+        __syncwarp();
+        ok = pass_to(ring0 + 2 * n);
+        continue;
+      }
+      auto qk = [&](int pos) {
+        const uint64_t dk = desc_k + static_cast<uint64_t>(pos % NS * (C::kSlotBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * kSubBytes + (k % 4) * 32;
-            mma_bf16_ss(tS[st], desc_kmajor_sw128(qa + off), desc_kmajor_sw128(ka + off), kIdescS,
-                        k > 0);
-          }
-        };
-        auto pv = [&](int st, int pos, bool acc) {
-          const uint32_t va = smem_u32(kv_smem + (pos % NS) * C::kSlotBytes);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ts(tO[st], tS[st] + k * 8, desc_mnmajor_sw128(va + k * 2048, kSubBytes),
-                        kIdescO, acc || k > 0);
-          uint32_t rest = *static_cast<volatile uint32_t*>(&b->heavy[st]);
-          rest |= rest >> 16;
-          rest = (rest | rest >> 8) & 0xffu;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            if ((rest >> k) & 1u)
-              mma_bf16_ts(tO[st], tS[st] + 64 + k * 8, desc_mnmajor_sw128(va + k * 2048, kSubBytes),
-                          kIdescO, 1);
-        };
-        auto probs = [&](int st) {                 // stream st's P is in TMEM
-          if (!wait_or_abort(&b->p_full[st], ph_p[st], b, a.dev_status)) return false;
-          ph_p[st] ^= 1;
-          tc_fence_after();
-          return true;
-        };
-        ok = wait_or_abort(&b->q_full, n_items & 1, b, a.dev_status);
+        for (int k = 0; k < D / 16; ++k) {
+          const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
+          mma_bf16_ss_warp(dS, dq + off, dk + off, kIdescS, k > 0);
+        }
+      };
+      // the next phase of s_full must not complete before the last one was seen
+      if (ended) {
+        ok = warp_wait(&b->o_seen[st], ph_o, b, a.dev_status);
         if (!ok) break;
+        ph_o ^= 1;
+      }
+      ended = true;
+      ok = own(ring0 + ring_k(pair, first));
+      if (!ok) break;
+      tc_fence_after();
+      qk(ring0 + ring_k(pair, first));
+      mma_commit_warp(&b->s_full[st]);
+      done(ring0 + ring_k(pair, first));
+      if (first + step >= n) mma_commit_warp(&b->q_empty);
+      for (int i = first; i < n; i += step) {
+        const int v_at = ring0 + ring_v(pair, n, i), k_at = ring0 + ring_k(pair, i + step);
+        const bool more = i + step < n;
+        ok = own(v_at) && (!more || own(k_at)) &&
+             warp_wait(&b->p_full[st], ph_p, b, a.dev_status);
+        if (!ok) break;
+        ph_p ^= 1;
         tc_fence_after();
-        if (pair) {
-          ok = full(ring0);
-          if (!ok) break;
-          qk(0, ring0);
-          mma_commit(&b->s_full[0]);
-          qk(1, ring0);
-          mma_commit(&b->s_full[1]);
-          mma_commit(&b->kv_empty[ring0 % NS]);
-          if (n == 1) mma_commit(&b->q_empty);
-          for (int j = 0; j < n && ok; ++j) {
-            const int pv_at = ring0 + 2 * j + 1, k_at = pv_at + 1;
-            const bool more = j + 1 < n;
-            ok = full(pv_at) && probs(0);
-            if (!ok) break;
-            pv(0, pv_at, j > 0 || b->o_init[0]);
-            if (more) {
-              ok = full(k_at);
-              if (!ok) break;
-              qk(0, k_at);
-            }
-            mma_commit(&b->s_full[0]);
-            ok = probs(1);
-            if (!ok) break;
-            pv(1, pv_at, j > 0 || b->o_init[1]);
-            mma_commit(&b->kv_empty[pv_at % NS]);
-            if (more) {
-              qk(1, k_at);
-              mma_commit(&b->kv_empty[k_at % NS]);
-              if (j + 2 == n) mma_commit(&b->q_empty);
-            }
-            mma_commit(&b->s_full[1]);
-          }
-        } else {
-          for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = full(ring0 + i);
-            if (!ok) break;
-            qk(i, ring0 + i);
-            mma_commit(&b->s_full[i]);
-            mma_commit(&b->kv_empty[(ring0 + i) % NS]);
-          }
-          if (n <= 2) mma_commit(&b->q_empty);
-          for (int i = 0; i < n && ok; ++i) {
-            const int st = i & 1, v_at = ring0 + ring_v(false, n, i);
-            ok = full(v_at) && probs(st);
-            if (!ok) break;
-            pv(st, v_at, i >= 2 || b->o_init[st]);
-            mma_commit(&b->kv_empty[v_at % NS]);
-            if (i + 2 < n) {
-              const int k_at = ring0 + ring_k(false, i + 2);
-              ok = full(k_at);
-              if (!ok) break;
-              qk(st, k_at);
-              mma_commit(&b->kv_empty[k_at % NS]);
-              if (i + 3 == n) mma_commit(&b->q_empty);
-            }
-            mma_commit(&b->s_full[st]);
+        const volatile Told* told = &b->told[st];
+        const uint32_t heavy = told->heavy;
+        const bool acc = i > first || told->o_init != 0;
+        const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_bf16_ts_warp(dO, dS + k * 8, dv + k * (2048 >> 4), kIdescO, acc || k > 0);
+        if (heavy != 0) {
+          // the remainders of P, for the warps that have one in the step
+#pragma unroll 1
+          for (int k = 0; k < kTile / 16; ++k) {
+            const uint32_t who = (heavy >> k) & 0x01010101u;
+            if (who == 0) continue;
+            const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
+                                     ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
+            mma_bf16_ts_warp_lanes(dO, dS + 64 + k * 8, dv + k * (2048 >> 4), kIdescO, off);
           }
         }
+        if (more) qk(k_at);
+        mma_commit_warp(&b->s_full[st]);
+        done(v_at);
+        if (more) {
+          done(k_at);
+          if (i + 2 * step >= n) mma_commit_warp(&b->q_empty);
+        }
       }
-      if (!ok) {
-        mma_commit(&b->drain);
-        mbar_wait_bounded(&b->drain, 0, kWaitLimitNs);
-      }
+      if (ok && !pair) ok = pass_to(ring0 + 2 * n);
     }
-    __syncwarp();
+    if (!ok) {
+      mma_commit_warp(&b->drain[st]);
+      mbar_wait_bounded(&b->drain[st], 0, kWaitLimitNs);
+      __syncwarp();
+    }
   } else if (warp == 10) {
     // ------------------------------------------------- value tiles at an edge
-    regs_lower<kRegsOther>();
     uint32_t raw_phase = 0;
     bool ok = true;
     for (int n_items = 0; ok; ++n_items) {
@@ -510,14 +590,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Item it = b->items[slot].it;
       const int ring0 = b->items[slot].ring0;
+      const int edge_lo = b->items[slot].edge_lo, edge_hi = b->items[slot].edge_hi;
       __syncwarp();
       if (it.ntiles == 0) break;
       if (lane == 0) mbar_arrive(&b->item_empty[slot]);
       const bool pair = it.nt > p.tok_tile;
       const Sight see = sight(a, it.kv, it.pos0, it.nt);
       for (int i = 0; i < it.ntiles && ok; ++i) {
+        if (it.tile0 + i >= edge_lo && it.tile0 + i < edge_hi) {
+          i = min(it.ntiles, edge_hi - it.tile0) - 1;       // on to the upper edge
+          continue;
+        }
         const TileSpan t = tile_span(p, it.tile0 + i);
-        if (!at_edge(t, see)) continue;
         const int s = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
         ok = warp_wait(&b->kv_raw[s], (raw_phase >> s) & 1, b, a.dev_status);
         if (!ok) break;
@@ -525,41 +609,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
         const int c1 = tile_col(p, t, see.all_lo), c2 = tile_col(p, t, see.all_hi);
         uint8_t* rows = kv_smem + s * C::kSlotBytes;
-        uint32_t found[4] = {0, 0, 0, 0};
-        // lanes 0 .. 8 kSub - 1 hold a row, 16 bytes each
+        if (lane < 4) b->poison[s][lane] = 0;
+        // kLanes lanes hold a row, 16 bytes each, kPer rows at a time
         constexpr int kLanes = 8 * C::kSub, kPer = 32 / kLanes;
-        const int sub = (lane % kLanes) / 8, unit = lane % 8;
-#pragma unroll 4
-        for (int n0 = 0; n0 < kTile; n0 += kPer) {
-          const int n = n0 + lane / kLanes;
-          uint4* at = reinterpret_cast<uint4*>(rows + sub * kSubBytes + n * 128 + unit * 16);
-          const bool dark = n < c0 || n >= c3;              // no row sees it
-          bool clear = dark;
-          if (!dark && (n < c1 || n >= c2)) {               // some rows see it
-            const uint4 x = *at;
-            auto odd = [](uint32_t u) {
-              return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-            };
-            clear = odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w);
-          }
-          const uint32_t who = __ballot_sync(0xffffffffu, clear);
-          const int first = lane / kLanes * kLanes;
-          const bool row_clear = ((who >> first) & bits_below(kLanes)) != 0;
-          if (row_clear) *at = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            if (n0 + j >= c0 && n0 + j < c3 && ((who >> (j * kLanes)) & bits_below(kLanes)))
-              found[(n0 + j) >> 5] |= 1u << ((n0 + j) & 31);
-        }
-        if (lane < 4)
-          b->poison[s][lane] = lane == 0 ? found[0] : lane == 1 ? found[1] : lane == 2 ? found[2]
-                                                                                    : found[3];
-        fence_proxy_async_smem();
+        const int my_row = lane / kLanes;
+        uint8_t* mine = rows + (lane % kLanes) / 8 * kSubBytes + lane % 8 * 16;
+        auto clear = [&](int lo, int hi) {                   // rows that no row sees
+          for (int n = lo + my_row; n < hi; n += kPer)
+            *reinterpret_cast<uint4*>(mine + n * 128) = make_uint4(0, 0, 0, 0);
+        };
+        clear(0, c0);
+        clear(c3, kTile);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->kv_full[s]);
+        auto scan = [&](int lo, int hi) {                    // rows that some rows see
+          constexpr int kU = 8;
+          for (int n0 = lo; n0 < hi; n0 += kPer * kU) {
+            uint4 v[kU];
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+              const int n = n0 + j * kPer + my_row;
+              v[j] = n < hi ? *reinterpret_cast<const uint4*>(mine + n * 128)
+                            : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+              auto odd = [](uint32_t u) {                    // an exponent of all ones
+                return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+              };
+              const uint32_t who = __ballot_sync(
+                  0xffffffffu, odd(v[j].x) || odd(v[j].y) || odd(v[j].z) || odd(v[j].w));
+              if (who == 0) continue;
+              const int n = n0 + j * kPer + my_row;
+              if ((who >> (my_row * kLanes)) & bits_below(kLanes)) {
+                *reinterpret_cast<uint4*>(mine + n * 128) = make_uint4(0, 0, 0, 0);
+                if (lane % kLanes == 0) atomicOr(&b->poison[s][n >> 5], 1u << (n & 31));
+              }
+            }
+          }
+        };
+        scan(c0, min(c1, c3));
+        scan(max(max(c0, c1), c2), c3);
+        fence_proxy_async_smem();
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) {
+          volatile int32_t* mended = b->mended;
+          if (pair || (i & 1) == 0) mended[0] = mended[0] + 1;
+          if (pair || (i & 1) == 1) mended[1] = mended[1] + 1;
+          mbar_arrive(&b->kv_full[s]);
+        }
       }
     }
-  } else if (warp < 8) {
+  }
+  } else {
     // -------------------------------------------------------------- softmax
     regs_raise<kRegsSoftmax>();
     const int st = warp >> 2;
@@ -569,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_tok = row / a.G, row_g = row - row_tok * a.G;
     const bool row_in_tile = row_tok < p.tok_tile;
     uint32_t ph_s = 0, ph_wg = 0, ph_ml = 0;
+    int32_t n_mended = 0;                         // value tiles of the stream at an edge so far
     int32_t* counters = static_cast<int32_t*>(a.workspace);
     float* slots =
         reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
@@ -581,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Item it = b->items[slot].it;
       const int ring0 = b->items[slot].ring0;
+      const int edge_lo = b->items[slot].edge_lo, edge_hi = b->items[slot].edge_hi;
       __syncwarp();
       if (it.ntiles == 0) break;
       if (lane == 0) mbar_arrive(&b->item_empty[slot]);
@@ -590,8 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_tok = min(p.tok_tile, it.nt - tok_off);
       const bool valid = row_in_tile && row_tok < n_tok;
       const bool busy = (warp & 3) * 32 < n_tok * a.G;      // any valid row in the warp
-      const Sight see = sight(a, it.kv, it.pos0 + tok_off, n_tok);
-      const Sight see_item = sight(a, it.kv, it.pos0, it.nt);
       const int pos = it.pos0 + tok_off + min(row_tok, n_tok - 1);
       const int key_hi = a.causal ? min(it.kv, pos + 1) : it.kv;
       const int key_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
@@ -602,18 +704,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&b->s_full[st], ph_s, b, a.dev_status);
         if (!ok) break;
         ph_s ^= 1;
+        const bool edge = it.tile0 + i < edge_lo || it.tile0 + i >= edge_hi;
+        n_mended += edge;
         if (busy) {
           tc_fence_after();
           uint32_t x[kTile];
 #pragma unroll
           for (int c = 0; c < kTile; c += 32) tmem_ld_32x32b_x32(sS + c, x + c);
           tmem_ld_wait();
-          const TileSpan t = tile_span(p, it.tile0 + i);
-          const bool whole = !p.has_holes && t.cnt == kTile && t.tok0 >= see.all_lo &&
-                             t.tok0 + kTile <= see.all_hi;
-          if (!whole) {
-            const int lo = tile_col(p, t, key_lo), hi = min(tile_col(p, t, key_hi),
-                                                            p.pages_tile == 1 ? t.cnt : kTile);
+          if (edge || p.ragged) {
+            const TileSpan t = tile_span(p, it.tile0 + i);
+            const int lo = tile_col(p, t, key_lo);
+            const int hi = min(tile_col(p, t, key_hi), p.has_holes ? kTile : t.cnt);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t keep =
@@ -623,15 +725,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!((keep >> j) & 1u)) x[32 * c + j] = 0xff800000u;      // -inf
             }
           }
+          auto sc = [&](int j) { return __uint_as_float(x[j]); };
           float mx[8];                                       // of each 16 keys
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            mx[g] = __uint_as_float(x[16 * g]);
+          for (int g = 0; g < 8; ++g) mx[g] = max3(sc(16 * g), sc(16 * g + 1), sc(16 * g + 2));
 #pragma unroll
-            for (int j = 1; j < 16; ++j) mx[g] = fmaxf(mx[g], __uint_as_float(x[16 * g + j]));
-          }
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+          for (int j = 3; j < 15; j += 2)
+#pragma unroll
+            for (int g = 0; g < 8; ++g) mx[g] = max3(mx[g], sc(16 * g + j), sc(16 * g + j + 1));
+#pragma unroll
+          for (int g = 0; g < 8; ++g) mx[g] = fmaxf(mx[g], sc(16 * g + 15));
+          const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
+                                 fmaxf(mx[6], mx[7])) *
                             a.scale_log2;
           const bool raise = top > m + kLag || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, raise)) {
@@ -639,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (raise) m = top;
             l *= f;
             if (k > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(sO + c, o);
@@ -651,50 +756,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          // steps in which a key has more than kHeavy of the row's sum so far
-          uint32_t heavy = 0xffu;
-          if (pair) {
-            const float least = __log2f(kHeavy * (l + exp2_fast(top - ref)));
-            heavy = 0;
+          // steps of 16 keys in which one has more than a share of the row's sum so far
+          uint32_t heavy = 0;
+          const float least =
+              __log2f((pair ? kHeavyPair : kHeavySingle) * (l + exp2_fast(top - ref)));
+          if (__any_sync(0xffffffffu, valid && top - ref > least)) {
 #pragma unroll
             for (int g = 0; g < 8; ++g)
               if (__any_sync(0xffffffffu, valid && fmaf(mx[g], a.scale_log2, -ref) > least))
                 heavy |= 1u << g;
           }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t sc_bits = __float_as_uint(a.scale_log2), ref_bits = __float_as_uint(-ref);
+          const uint64_t scale2 = pack_f32x2(sc_bits, sc_bits);
+          const uint64_t ref2 = pack_f32x2(ref_bits, ref_bits);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            uint32_t rest[8];
+            float e[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int e = 16 * g + 2 * j;
-              const float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), a.scale_log2, -ref));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), a.scale_log2, -ref));
-              sum[j & 3] += p0 + p1;
-              const uint32_t u = pack_bf16(p0, p1);
-              x[e >> 1] = u;
-              rest[j] = 0;
-              if ((heavy >> g) & 1u)
-                rest[j] = pack_bf16(p0 - __uint_as_float(u << 16),
-                                    p1 - __uint_as_float(u & 0xffff0000u));
+            for (int j = 0; j < 16; j += 2) {
+              const int n = 16 * g + j;
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[n], x[n + 1]), scale2, ref2), e[j], e[j + 1]);
+              e[j] = exp2_fast(e[j]);
+              e[j + 1] = exp2_fast(e[j + 1]);
+              sum[(j >> 1) & 3] =
+                  add_f32x2(sum[(j >> 1) & 3],
+                            pack_f32x2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
+              x[n >> 1] = pack_bf16(e[j], e[j + 1]);
             }
-            tmem_st_32x32b_x8(sS + 64 + 8 * g, rest);
+            if ((heavy >> g) & 1u) {
+              uint32_t rest[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t u = x[8 * g + j];
+                rest[j] = pack_bf16(e[2 * j] - __uint_as_float(u << 16),
+                                    e[2 * j + 1] - __uint_as_float(u & 0xffff0000u));
+              }
+              tmem_st_32x32b_x8(sS + 64 + 8 * g, rest);
+            }
+            if (g == 3) tmem_st_32x32b_x32(sS, x);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st_32x32b_x32(sS, x);
           tmem_st_32x32b_x32(sS + 32, x + 32);
-          if (lane == 0) reinterpret_cast<volatile uint8_t*>(&b->heavy[st])[warp & 3] = heavy;
+          {
+            float s0, s1;
+            unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+            l += s0 + s1;
+          }
+          if (lane == 0)
+            reinterpret_cast<volatile uint8_t*>(&b->told[st].heavy)[warp & 3] = heavy;
           tmem_st_wait();
 
           bool init = false;
-          if (at_edge(t, see_item)) {
+          if (edge) {
+            const TileSpan t = tile_span(p, it.tile0 + i);
             // rare: value rows that were cleared although some rows see them
             const int pos_v = ring0 + ring_v(pair, it.ntiles, i);
-            ok = warp_wait(&b->kv_full[pos_v % NS], (pos_v / NS) & 1, b, a.dev_status);
+            ok = warp_wait_count(&b->mended[st], n_mended, b, a.dev_status);
             if (!ok) break;
-            for (int n = 0; n < kTile; ++n) {
-              if (!((b->poison[pos_v % NS][n >> 5] >> (n & 31)) & 1u)) continue;
-              const int tok = tile_tok(p, t, n), blk = tok / a.B;
+            uint32_t left = 0;
+            for (int n = -1;;) {
+              // the next set bit, in order
+              while (left == 0 && (n >> 5) < 3) {
+                n = ((n >> 5) + 1) << 5;
+                left = b->poison[pos_v % NS][n >> 5];
+              }
+              if (left == 0) break;
+              n = (n & ~31) + __ffs(left) - 1;
+              left &= left - 1;
+              const int tok = tile_tok(p, t, n), blk = fast_div(tok, p.page);
               const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
               const uint32_t two = tmem_ld_32x32b_x1(sS + (n >> 1));
               tmem_ld_wait();
@@ -720,10 +849,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               init = true;
             }
           }
-          if (k == 0 && (warp & 3) == 0 && lane == 0) b->o_init[st] = init ? 1 : 0;
+          if (k == 0 && (warp & 3) == 0 && lane == 0) b->told[st].o_init = init ? 1 : 0;
           tc_fence_before();
         } else if (lane == 0) {
-          reinterpret_cast<volatile uint8_t*>(&b->heavy[st])[warp & 3] = 0;
+          reinterpret_cast<volatile uint8_t*>(&b->told[st].heavy)[warp & 3] = 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->p_full[st]);
@@ -734,6 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ph_s ^= 1;
         tc_fence_after();
+        if (lane == 0) mbar_arrive(&b->o_seen[st]);
+        __syncwarp();
       }
 
       // single mode: stream 0 joins the two streams' rows
@@ -772,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = slots + (static_cast<size_t>(blockIdx.x) * 2 + slot_of(it.part)) * slot_n;
       if (busy) {
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + q_row * a.o_tok + head * a.o_head;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(sO + c, o);
@@ -802,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(part + slot_row * D + c + j) =
+              *reinterpret_cast<uint4*>(part + ((c + j) / 4 * kSlotRows + slot_row) * 4) =
                   make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
         }
@@ -838,47 +969,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!b->last[st]) continue;
       __threadfence();
       if (row == 0) counters[2 * it.cta0 + st] = 0;
-      const int rows = n_tok * a.G, base = pair ? st * kRowsM : 0;
-      constexpr int kDv = D / 4;
-      for (int e = row; e < rows * kDv; e += 128) {
-        const int er = e / kDv, col = (e - er * kDv) * 4;
-        float M = -INFINITY;
-        for (int q = 0; q < it.nparts; ++q) {
-          const float* ps = slots + (static_cast<size_t>(it.cta0 + q) * 2 + slot_of(q)) * slot_n;
-          M = fmaxf(M, __ldcg(ps + kSlotRows * D + base + er));
-        }
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = 0; q < it.nparts; ++q) {
-          const float* ps = slots + (static_cast<size_t>(it.cta0 + q) * 2 + slot_of(q)) * slot_n;
-          const float pm = __ldcg(ps + kSlotRows * D + base + er);
-          const float pl = __ldcg(ps + kSlotRows * D + kSlotRows + base + er);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + (base + er) * D + col));
-          if (pl == 0.f) continue;
-          const float f = part_weight(pm, pl, M);
-          L = fmaf(pl, f, L);
-          acc.x = fmaf(v.x, f, acc.x);
-          acc.y = fmaf(v.y, f, acc.y);
-          acc.z = fmaf(v.z, f, acc.z);
-          acc.w = fmaf(v.w, f, acc.w);
-        }
-        const float r = 1.f / L;
-        const int tok = er / a.G, hd = it.h * a.G + er - tok * a.G;
-        const int64_t orow = it.q0 + tok_off + tok;
-        uint2 u = make_uint2(0, 0);
-        if (L != 0.f) {
-          u.x = pack_bf16(acc.x * r, acc.y * r);
-          u.y = pack_bf16(acc.z * r, acc.w * r);
-        }
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.o_tok +
-                                  hd * a.o_head + col) = u;
-        if (a.lse != nullptr && col == 0)
-          a.lse[orow * (a.H * a.G) + hd] =
-              L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-      }
+      join_parts(slots, slot_n, kSlotRows, pair ? st * kRowsM : 0, D, it, n_tok * a.G, row, 128,
+                 [&](int r, int col, float4 v, float lse) {
+                   const int tok = r / a.G, hd = it.h * a.G + r - tok * a.G;
+                   const int64_t orow = it.q0 + tok_off + tok;
+                   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.o_tok +
+                                             hd * a.o_head + col) =
+                       make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                   if (a.lse != nullptr && col == 0) a.lse[orow * (a.H * a.G) + hd] = lse;
+                 });
     }
-  } else {
-    regs_lower<kRegsOther>();                     // a warpgroup moves its registers together
   }
 
   tc_fence_before();
@@ -925,10 +1025,16 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   s.kv_cap = a.width * a.B;
   s.causal = a.causal;
   s.window = a.window;
-  s.tok_item = 2 * p.tok_tile;
-  s.group_tok = a.B < kTile ? p.pages_tile * a.B : a.B;
+  const int group = a.B < kTile ? p.pages_tile * a.B : a.B;
+  s.item = make_fastdiv(2 * p.tok_tile);
+  s.group = make_fastdiv(group);
   s.group_tiles = a.B < kTile ? 1 : (a.B + kTile - 1) / kTile;
-  s.tile_tok = a.B < kTile ? s.group_tok : kTile;
+  s.tile = make_fastdiv(a.B < kTile ? group : kTile);
+  s.even = s.group_tiles == 1 || a.B % kTile == 0;
+  p.ragged = p.has_holes || (a.B > kTile && a.B % kTile != 0);
+  p.page = make_fastdiv(a.B);
+  p.rows = make_fastdiv(p.page_rows);
+  p.tiles = make_fastdiv(s.group_tiles);
 
   TcMaps maps;
   std::memset(&maps, 0, sizeof(maps));
