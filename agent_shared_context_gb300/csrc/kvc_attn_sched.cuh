@@ -104,7 +104,7 @@ __device__ __forceinline__ int n_items(const SchedArgs& a, const Request& q) {
 
 // sum over 0 <= i < n of floor((a i + b) / m), by the steps of Euclid's
 // algorithm on (a, m).
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+static __device__ __noinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t s = 0;
   while (n > 0) {
     if (a >= m) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 // Units of the request's first `n` items of one KV head.  A plain causal chunk
 // (every chunk without a window, on pages that fill their tiles) has a closed
 // form: item i sees ceil((pos0 + (i + 1) item) / tile) tiles.
-__device__ __forceinline__ int64_t first_units(const SchedArgs& a, const Request& q, int n) {
+static __device__ __noinline__ int64_t first_units(const SchedArgs& a, const Request& q, int n) {
   if (n <= 0) return 0;
   if (a.even && a.window == 0 && n > 2) {
     const int64_t last = item_units(a, q, n - 1);      // the last may be shorter than an item
@@ -157,28 +157,42 @@ struct Shared {
   int32_t item_off;    // units of that item before the share
 };
 
-// CTA that owns unit u when U units are cut into n shares [c U / n, (c+1) U / n).
-__device__ __forceinline__ int owner_of(int64_t u, int64_t U, int n) {
-  const int64_t x = (u + 1) * n - 1;
-  if (x < (int64_t(1) << 32) && U < (int64_t(1) << 32))
-    return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(U));
-  return static_cast<int>(x / U);
+// Calls, not copies: the kernels' instruction footprint is a cost of its own
+// (their first pass through the code misses every cache).
+static __device__ __noinline__ int64_t div64(int64_t x, int64_t y) {
+  if (x < (int64_t(1) << 32) && y < (int64_t(1) << 32))
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
-__device__ __forceinline__ int64_t share_start(int c, int64_t U, int n) {
-  const int64_t x = c * U;
-  if (x < (int64_t(1) << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(n);
-  return x / n;
-}
+// U units cut into n shares [c U / n, (c + 1) U / n).
+struct Shares {
+  int64_t U, q;                // all units, U / n
+  int32_t n, rem;              // shares, U % n
+  float n_over_U;
+
+  __device__ __forceinline__ int64_t start(int c) const {
+    return c * q + static_cast<uint32_t>(c * rem) / static_cast<uint32_t>(n);
+  }
+  // The share of unit u: an estimate, then a step or two to the exact one.
+  __device__ __forceinline__ int owner(int64_t u) const {
+    int c = min(n - 1, static_cast<int>(static_cast<float>(u) * n_over_U));
+#pragma unroll 1
+    while (c > 0 && start(c) > u) --c;
+#pragma unroll 1
+    while (c + 1 < n && start(c + 1) <= u) ++c;
+    return c;
+  }
+};
 
 // Walks the share of one CTA.  All threads that walk hold the same state.
 struct Walker {
-  int64_t U, u, u1;            // all units, the next one, the end of the share
+  Shares sh;
+  int64_t u, u1;               // the next unit, the end of the share
   int32_t r, h, i;             // where the next unit lies
   int64_t item_u0;             // first unit of that item
   Request q;
   int32_t n;                   // items of request r
-  int32_t grid;
 
   // Next part of the share; false at its end.
   __device__ __forceinline__ bool next(const SchedArgs& a, Item* out) {
@@ -200,10 +214,11 @@ struct Walker {
           out->pos0 = q.pos0 + t0;
           out->tile0 = lo + static_cast<int>(u - item_u0);
           out->ntiles = static_cast<int>(stop - u);
-          const int c0 = owner_of(item_u0, U, grid);
+          const int me = blockIdx.x;
+          const int c0 = u == item_u0 ? me : sh.owner(item_u0);
           out->cta0 = c0;
-          out->part = static_cast<int>(blockIdx.x) - c0;
-          out->nparts = owner_of(end - 1, U, grid) - c0 + 1;
+          out->part = me - c0;
+          out->nparts = (end <= u1 ? me : sh.owner(end - 1)) - c0 + 1;
           u = stop;
           return true;
         }
@@ -267,15 +282,18 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
   // no empty shares between others: an item's parts are consecutive CTAs
   const int n = static_cast<int>(U < gridDim.x ? U : gridDim.x);
   Walker w;
-  w.U = U;
-  w.grid = n;
+  w.sh.U = U;
+  w.sh.n = n;
+  w.sh.q = n > 0 ? div64(U, n) : 0;
+  w.sh.rem = static_cast<int>(U - w.sh.q * n);
+  w.sh.n_over_U = U > 0 ? static_cast<float>(n) / static_cast<float>(U) : 0.f;
   w.u = w.u1 = w.item_u0 = U;
   w.r = a.R;
   w.h = w.i = w.n = 0;
   w.q = Request{0, 0, 0, 0};
   if (static_cast<int>(blockIdx.x) >= n) return w;
-  w.u = share_start(blockIdx.x, U, n);
-  w.u1 = share_start(blockIdx.x + 1, U, n);
+  w.u = w.sh.start(blockIdx.x);
+  w.u1 = w.sh.start(blockIdx.x + 1);
   // the request of unit u ...
   int64_t before = 0;
   for (int base = 0; base < a.R; base += THREADS) {
@@ -291,9 +309,9 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
     }
     if (before + incl > w.u && before + incl - mine <= w.u) {   // one thread
       const int64_t off = w.u - (before + incl - mine);
-      const int64_t hu = mine / a.H;
+      const int64_t hu = div64(mine, a.H);
       sh->r = r;
-      sh->h = static_cast<int>(off / hu);
+      sh->h = static_cast<int>(div64(off, hu));
       sh->off = off - sh->h * hu;
     }
     before += total;
@@ -357,19 +375,21 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
   if (span > n_threads) span = n_threads;
   const int d4 = d / 4, step = n_threads / span;
   const float* base = slots + static_cast<size_t>(it.cta0) * 2 * slot_n;
+#pragma unroll 1
   for (int row = tid & (span - 1); row < rows; row += span) {
     auto part = [&](int p) { return base + (static_cast<size_t>(p) * 2 + slot_of(p)) * slot_n; };
     float M = -INFINITY;
-#pragma unroll 8
+#pragma unroll 4
     for (int p = 0; p < it.nparts; ++p)
       M = fmaxf(M, __ldcg(part(p) + slot_rows * d + row0 + row));
     constexpr int kC = 8;
+#pragma unroll 1
     for (int c0 = tid / span; c0 < d4; c0 += kC * step) {
       float4 acc[kC];
       float L = 0.f;
 #pragma unroll
       for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
       for (int p = 0; p < it.nparts; ++p) {
         const float* ps = part(p);
         const float m = __ldcg(ps + slot_rows * d + row0 + row);

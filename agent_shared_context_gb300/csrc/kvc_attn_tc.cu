@@ -42,7 +42,7 @@
 // The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
 // 2^-8 average out over many keys of like weight but not where few carry a
 // row, so the remainder P - bf16(P) is multiplied too, in the steps of 16 keys
-// in which some row has a key with more than 1/8 of its sum so far (1/16 in
+// in which some row has a key with more than 1/5 of its sum so far (1/16 in
 // single mode, which waits for memory anyway): few steps of a long context.  S
 // leaves room for it in TMEM, beside P.
 //
@@ -74,7 +74,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kItems = 4;                  // depth of the item ring
 constexpr int kNoPage = INT32_MIN;         // no key there: read as zeros
 constexpr float kLag = 8.0f;               // log2 by which m may lag behind
-constexpr float kHeavyPair = 0.125f;       // share of a row's sum that makes a key heavy
+constexpr float kHeavyPair = 0.2f;         // share of a row's sum that makes a key heavy
 constexpr float kHeavySingle = 0.0625f;
 
 template <int D>
@@ -119,6 +119,7 @@ struct Bars {
   uint64_t kv_full[NS], kv_raw[NS], kv_empty[NS];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2];
+  uint64_t turn[2];                // pair mode: whose MMAs are issued next
   uint64_t o_seen[2];              // the stream's warps know that an item's O is complete
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t ml_full, ml_empty;      // stream 1's row statistics for stream 0
@@ -135,47 +136,51 @@ struct Bars {
   Shared sched;
 };
 
-template <int NS>
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Bars<NS>* b,
-                                              int32_t* dev_status) {
-  if (mbar_wait_polling(bar, parity, kWaitLimitNs, &b->abort_flag)) return true;
-  volatile int32_t* ab = &b->abort_flag;
-  if (*ab == 0) {
-    *ab = 1;
-    atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_DEVICE_TIMEOUT));
-  }
-  return false;
-}
-
-// Waits until *count, which another warp raises, has reached `want`.
-template <int NS>
-__device__ __forceinline__ bool warp_wait_count(const int32_t* count, int32_t want, Bars<NS>* b,
-                                                int32_t* dev_status) {
-  const volatile int32_t* c = count;
-  volatile int32_t* ab = &b->abort_flag;
+// Counts the polls of a wait: every 4,096 of them it looks at the timer, which
+// costs hundreds of cycles, and at the abort flag, which it raises at the limit.
+struct Patience {
   uint64_t t0 = 0;
-  bool ok = true;
-  for (uint32_t i = 1; *c - want < 0; ++i) {
-    if ((i & 4095u) != 0u) continue;
+  uint32_t polls = 0;
+  __device__ __forceinline__ bool out(int32_t* abort_flag) {
+    if ((++polls & 4095u) != 0u) return false;
+    volatile int32_t* flag = abort_flag;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
-    if (*ab == 0 && t - t0 <= kWaitLimitNs) continue;
-    if (*ab == 0) {
-      *ab = 1;
-      atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_DEVICE_TIMEOUT));
-    }
-    ok = false;
-    break;
+    if (t - t0 > kWaitLimitNs) *flag = 1;
+    return *flag != 0;
   }
-  __threadfence_block();
+};
+
+// A whole warp waits for a phase: all lanes give up together.
+template <int NS>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b) {
+  Patience p;
+  bool ok = true;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (p.out(&b->abort_flag)) {
+      ok = false;
+      break;
+    }
+  }
   return __all_sync(0xffffffffu, ok);
 }
 
-// A bounded wait of a whole warp: all lanes give up together.
+// A whole warp waits until *count, which another warp raises, has reached `want`.
 template <int NS>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b,
-                                          int32_t* dev_status) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, b, dev_status));
+__device__ __forceinline__ bool warp_wait_count(const volatile int32_t* count, int32_t want,
+                                                Bars<NS>* b) {
+  Patience p;
+  bool ok = true;
+#pragma unroll 1
+  while (*count - want < 0) {
+    if (p.out(&b->abort_flag)) {
+      ok = false;
+      break;
+    }
+  }
+  __threadfence_block();
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -289,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b->s_full[i], 1);
       mbar_init(&b->p_full[i], 4);
       mbar_init(&b->o_seen[i], 4);
+      mbar_init(&b->turn[i], 1);
       mbar_init(&b->wg[i], 4);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       const bool more = w.next(p.s, &it);
       const int slot = n_items % kItems;
-      ok = warp_wait(&b->item_empty[slot], ((n_items / kItems) & 1) ^ 1, b, a.dev_status);
+      ok = warp_wait(&b->item_empty[slot], ((n_items / kItems) & 1) ^ 1, b);
       if (!ok) break;
       if (!more) it.ntiles = 0;
       int edge_lo = 0, edge_hi = 0;
@@ -364,30 +370,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool pair = it.nt > p.tok_tile;
 
       // The pages of the lane's boxes of key tiles 0, 1, ... in order (`blk`,
-      // `sub`: page and tile in it).  A box beyond the pool (page P) is filled with 0.
+      // `sub`: page and tile in it), fetched one tile ahead.  A box beyond the pool
+      // (page P) is filled with 0.
       const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
       const int last_blk = it.kv > 0 ? fast_div(it.kv - 1, p.page) : -1;
-      int blk, sub = 0;
+      const int blk_step = p.pages_tile == 1 ? 1 : p.pages_tile;
+      int blk = it.tile0 * p.pages_tile + my_page, sub = 0;
       if (p.pages_tile == 1) {
         blk = fast_div(it.tile0, p.tiles);
         sub = it.tile0 - blk * p.s.group_tiles;
-      } else {
-        blk = it.tile0 * p.pages_tile + my_page;
       }
-      auto next_page = [&]() -> int {              // unchecked: looked at when it is used
-        const int page = lane < boxes && blk <= last_blk ? __ldg(table + blk) : kNoPage;
-        if (p.pages_tile > 1) {
-          blk += p.pages_tile;
-        } else if (++sub == p.s.group_tiles) {
-          sub = 0;
-          ++blk;
-        }
-        return page;
-      };
-      int pg0 = next_page(), pg1 = next_page();
+      auto fetch = [&]() { return lane < boxes && blk <= last_blk ? __ldg(table + blk) : kNoPage; };
+      int ahead = fetch(), page = 0, page_before = 0;       // of the next, the last two K tiles
+      int row_k = sub * kTile, row_v = row_k;               // first row of the tile in its page
+      const int row_end = p.s.group_tiles * kTile;
 
       // Q: one box per row tile and 64 columns
-      ok = warp_wait(&b->q_empty, (n_items & 1) ^ 1, b, a.dev_status);
+      ok = warp_wait(&b->q_empty, (n_items & 1) ^ 1, b);
       if (!ok) break;
       if (lane == 0) {
         const int tiles = pair ? 2 : 1;
@@ -400,52 +399,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++n_items;
 
-      int row_k = 0, row_v = 0;                    // first row of the tile in its page
-      if (p.pages_tile == 1)
-        row_k = row_v = (it.tile0 - fast_div(it.tile0, p.tiles) * p.s.group_tiles) * kTile;
-      const int row_end = p.pages_tile == 1 ? p.s.group_tiles * kTile : kTile;
-      auto load = [&](const CUtensorMap* map, int page, int& row, bool mend) -> bool {
-        uint64_t* bar = mend ? &b->kv_raw[s] : &b->kv_full[s];
-        if (!warp_wait(&b->kv_empty[s], wrap, b, a.dev_status)) return false;
-        if (page < 0 || page >= a.P) {
-          bad_page |= page != kNoPage;
-          page = a.P;
+      const int n = it.ntiles;
+      int i_k = 0, i_v = 0;                        // next tiles
+#pragma unroll 1
+      for (int pos = 0; pos < 2 * n; ++pos) {
+        // the order in which the MMAs take them: ring_k, ring_v
+        const bool is_v = pos == 2 * n - 1 || (pair ? (pos & 1) : pos >= 2 && !(pos & 1));
+        bool mend = false;
+        int use, row;
+        if (is_v) {
+          const int tile = it.tile0 + i_v;
+          mend = tile < edge_lo || tile >= edge_hi;
+          use = i_v + 1 == i_k ? page : page_before;
+          ++i_v;
+          row = row_v;
+          row_v = row + kTile == row_end ? 0 : row + kTile;
+        } else {
+          page_before = page;
+          page = ahead;
+          if (++sub == p.s.group_tiles) {
+            sub = 0;
+            blk += blk_step;
+          }
+          ahead = fetch();
+          if (page < 0 || page >= a.P) {
+            bad_page |= page != kNoPage;
+            page = a.P;
+          }
+          use = page;
+          ++i_k;
+          row = row_k;
+          row_k = row + kTile == row_end ? 0 : row + kTile;
         }
+        uint64_t* bar = mend ? &b->kv_raw[s] : &b->kv_full[s];
+        ok = warp_wait(&b->kv_empty[s], wrap, b);
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
         __syncwarp();
         if (lane < boxes)
-          tma_load_5d(my_dst + s * C::kSlotBytes, map, bar, my_sub * 64, row, it.h, a.layer, page);
-        row += kTile;
-        if (row == row_end) row = 0;
+          tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64, row,
+                      it.h, a.layer, use);
         raw_open = mend ? raw_open | 1u << s : raw_open & ~(1u << s);
         raw_phase ^= static_cast<uint32_t>(mend) << s;
         ++ring;
         if (++s == NS) {
           s = 0;
           wrap ^= 1;
-        }
-        return true;
-      };
-      const int n = it.ntiles;
-      auto load_k = [&](int page) { return load(&maps.k, page, row_k, false); };
-      auto load_v = [&](int page, int i) {
-        const int tile = it.tile0 + i;
-        return load(&maps.v, page, row_v, tile < edge_lo || tile >= edge_hi);
-      };
-      if (pair) {
-        for (int i = 0; i < n && ok; ++i) {
-          const int pg2 = next_page();
-          ok = load_k(pg0) && load_v(pg0, i);
-          pg0 = pg1;
-          pg1 = pg2;
-        }
-      } else {
-        ok = load_k(pg0) && (n == 1 || load_k(pg1));
-        for (int i = 0; i < n && ok; ++i) {
-          const int pg2 = next_page();
-          ok = load_v(pg0, i) && (i + 2 >= n || load_k(pg2));
-          pg0 = pg1;
-          pg1 = pg2;
         }
       }
       if (!ok) break;
@@ -474,11 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc_k = desc_kmajor_sw128(smem_u32(kv_smem));
     const uint64_t desc_v = desc_mnmajor_sw128(smem_u32(kv_smem), kSubBytes);
     uint32_t ph_p = 0, ph_o = 0;
+    uint32_t ph_turn = st == 0 ? 1 : 0;            // stream 0 begins
     bool ended = false;                            // an item's O may not be seen yet
     bool ok = true;
     for (int n_items = 0; ok; ++n_items) {
       const int slot = n_items % kItems;
-      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b);
       if (!ok) break;
       const int n = __shfl_sync(0xffffffffu, b->items[slot].it.ntiles, 0);
       if (n == 0) break;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Both MMA warps see every tile of the ring pass, in its order, and both free
       // every slot: a wait on a parity is only good for the next phase.
       auto full = [&](int pos) {
-        return warp_wait(&b->kv_full[pos % NS], (pos / NS) & 1, b, a.dev_status);
+        return warp_wait(&b->kv_full[pos % NS], (pos / NS) & 1, b);
       };
       int seen = ring0;                            // single mode: next position not seen
       auto pass_to = [&](int pos) {                // tiles of the other stream
@@ -508,8 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         seen = pos + 1;
         return full(pos);
       };
-      auto done = [&](int pos) { mma_commit_warp(&b->kv_empty[pos % NS]); };
-      ok = warp_wait(&b->q_full, n_items & 1, b, a.dev_status);
+      ok = warp_wait(&b->q_full, n_items & 1, b);
       if (!ok) break;
       if (first >= n) {                            // single mode, one tile: none for stream 1
         if (lane == 0) mbar_arrive(&b->q_empty);
@@ -517,61 +516,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = pass_to(ring0 + 2 * n);
         continue;
       }
-      auto qk = [&](int pos) {
-        const uint64_t dk = desc_k + static_cast<uint64_t>(pos % NS * (C::kSlotBytes >> 4));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
-          mma_bf16_ss_warp(dS, dq + off, dk + off, kIdescS, k > 0);
-        }
-      };
       // the next phase of s_full must not complete before the last one was seen
       if (ended) {
-        ok = warp_wait(&b->o_seen[st], ph_o, b, a.dev_status);
+        ok = warp_wait(&b->o_seen[st], ph_o, b);
         if (!ok) break;
         ph_o ^= 1;
       }
       ended = true;
-      ok = own(ring0 + ring_k(pair, first));
-      if (!ok) break;
-      tc_fence_after();
-      qk(ring0 + ring_k(pair, first));
-      mma_commit_warp(&b->s_full[st]);
-      done(ring0 + ring_k(pair, first));
-      if (first + step >= n) mma_commit_warp(&b->q_empty);
-      for (int i = first; i < n; i += step) {
-        const int v_at = ring0 + ring_v(pair, n, i), k_at = ring0 + ring_k(pair, i + step);
-        const bool more = i + step < n;
-        ok = own(v_at) && (!more || own(k_at)) &&
-             warp_wait(&b->p_full[st], ph_p, b, a.dev_status);
-        if (!ok) break;
-        ph_p ^= 1;
-        tc_fence_after();
-        const volatile Told* told = &b->told[st];
-        const uint32_t heavy = told->heavy;
-        const bool acc = i > first || told->o_init != 0;
-        const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_bf16_ts_warp(dO, dS + k * 8, dv + k * (2048 >> 4), kIdescO, acc || k > 0);
-        if (heavy != 0) {
-          // the remainders of P, for the warps that have one in the step
+      // per turn: O += P V of the tile before, then S of tile i
 #pragma unroll 1
-          for (int k = 0; k < kTile / 16; ++k) {
-            const uint32_t who = (heavy >> k) & 0x01010101u;
-            if (who == 0) continue;
-            const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
-                                     ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
-            mma_bf16_ts_warp_lanes(dO, dS + 64 + k * 8, dv + k * (2048 >> 4), kIdescO, off);
+      for (int i = first;; i += step) {
+        const bool pv = i > first, more = i < n;
+        const int v_at = ring0 + ring_v(pair, n, i - step), k_at = ring0 + ring_k(pair, i);
+        ok = (!pv || own(v_at)) && (!more || own(k_at)) &&
+             (!pv || warp_wait(&b->p_full[st], ph_p, b));
+        // In pair mode the streams take turns: were their MMAs to mix, both would get
+        // their scores late and together, and the tensor core would idle meanwhile.
+        if (ok && pair) {
+          ok = warp_wait(&b->turn[st], ph_turn, b);
+          ph_turn ^= 1;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (pv) {
+          ph_p ^= 1;
+          const volatile Told* told = &b->told[st];
+          const uint32_t heavy = told->heavy;
+          const bool acc = i > first + step || told->o_init != 0;
+          const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16_ts_warp(dO, dS + k * 8, dv + k * (2048 >> 4), kIdescO, acc || k > 0);
+          if (heavy != 0) {
+            // the remainders of P, for the warps that have one in the step
+#pragma unroll 1
+            for (int k = 0; k < kTile / 16; ++k) {
+              const uint32_t who = (heavy >> k) & 0x01010101u;
+              if (who == 0) continue;
+              const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
+                                       ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
+              mma_bf16_ts_warp_lanes(dO, dS + 64 + k * 8, dv + k * (2048 >> 4), kIdescO, off);
+            }
           }
         }
-        if (more) qk(k_at);
-        mma_commit_warp(&b->s_full[st]);
-        done(v_at);
         if (more) {
-          done(k_at);
-          if (i + 2 * step >= n) mma_commit_warp(&b->q_empty);
+          const uint64_t dk = desc_k + static_cast<uint64_t>(k_at % NS * (C::kSlotBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
+            mma_bf16_ss_warp(dS, dq + off, dk + off, kIdescS, k > 0);
+          }
         }
+        mma_commit_warp(&b->s_full[st]);
+        if (pair && lane == 0) mbar_arrive(&b->turn[st ^ 1]);
+        __syncwarp();
+        if (pv) mma_commit_warp(&b->kv_empty[v_at % NS]);
+        if (!more) break;
+        mma_commit_warp(&b->kv_empty[k_at % NS]);
+        if (i + step >= n) mma_commit_warp(&b->q_empty);
       }
       if (ok && !pair) ok = pass_to(ring0 + 2 * n);
     }
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int n_items = 0; ok; ++n_items) {
       const int slot = n_items % kItems;
-      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b);
       if (!ok) break;
       const Item it = b->items[slot].it;
       const int ring0 = b->items[slot].ring0;
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const TileSpan t = tile_span(p, it.tile0 + i);
         const int s = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
-        ok = warp_wait(&b->kv_raw[s], (raw_phase >> s) & 1, b, a.dev_status);
+        ok = warp_wait(&b->kv_raw[s], (raw_phase >> s) & 1, b);
         if (!ok) break;
         raw_phase ^= 1u << s;
         const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
@@ -614,15 +616,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kLanes = 8 * C::kSub, kPer = 32 / kLanes;
         const int my_row = lane / kLanes;
         uint8_t* mine = rows + (lane % kLanes) / 8 * kSubBytes + lane % 8 * 16;
-        auto clear = [&](int lo, int hi) {                   // rows that no row sees
-          for (int n = lo + my_row; n < hi; n += kPer)
+        // rows that no row sees: [0, c0), [c3, 128)
+#pragma unroll 1
+        for (int n = my_row; n < kTile; n += kPer)
+          if (n < c0 || n >= c3)
             *reinterpret_cast<uint4*>(mine + n * 128) = make_uint4(0, 0, 0, 0);
-        };
-        clear(0, c0);
-        clear(c3, kTile);
         __syncwarp();
-        auto scan = [&](int lo, int hi) {                    // rows that some rows see
-          constexpr int kU = 8;
+        // rows that some rows see: [c0, c1), [c2, c3)
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          const int lo = part == 0 ? c0 : max(max(c0, c1), c2), hi = part == 0 ? min(c1, c3) : c3;
+          constexpr int kU = 4;
+#pragma unroll 1
           for (int n0 = lo; n0 < hi; n0 += kPer * kU) {
             uint4 v[kU];
 #pragma unroll
@@ -646,9 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-        };
-        scan(c0, min(c1, c3));
-        scan(max(max(c0, c1), c2), c3);
+        }
         fence_proxy_async_smem();
         __threadfence_block();
         __syncwarp();
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (int n_items = 0; ok; ++n_items) {
       const int slot = n_items % kItems;
-      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b, a.dev_status);
+      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b);
       if (!ok) break;
       const Item it = b->items[slot].it;
       const int ring0 = b->items[slot].ring0;
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       for (int k = 0; k < n_st; ++k) {
         const int i = pair ? k : 2 * k + st;                // key tile of the item
-        ok = warp_wait(&b->s_full[st], ph_s, b, a.dev_status);
+        ok = warp_wait(&b->s_full[st], ph_s, b);
         if (!ok) break;
         ph_s ^= 1;
         const bool edge = it.tile0 + i < edge_lo || it.tile0 + i >= edge_hi;
@@ -756,45 +759,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          // steps of 16 keys in which one has more than a share of the row's sum so far
-          uint32_t heavy = 0;
-          const float least =
-              __log2f((pair ? kHeavyPair : kHeavySingle) * (l + exp2_fast(top - ref)));
-          if (__any_sync(0xffffffffu, valid && top - ref > least)) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              if (__any_sync(0xffffffffu, valid && fmaf(mx[g], a.scale_log2, -ref) > least))
-                heavy |= 1u << g;
-          }
           const uint32_t sc_bits = __float_as_uint(a.scale_log2), ref_bits = __float_as_uint(-ref);
           const uint64_t scale2 = pack_f32x2(sc_bits, sc_bits);
           const uint64_t ref2 = pack_f32x2(ref_bits, ref_bits);
+          // steps of 16 keys in which one has more than a share of the row's sum so far
+          uint32_t heavy = 0;
+          const float p_top = exp2_fast(top - ref);
+          const float least = (pair ? kHeavyPair : kHeavySingle) * (l + p_top);
+          if (__any_sync(0xffffffffu, valid && p_top > least)) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              if (__any_sync(0xffffffffu,
+                             valid && exp2_fast(fmaf(mx[g], a.scale_log2, -ref)) > least))
+                heavy |= 1u << g;
+          }
+          // P, and its remainder where it is wanted, in passes without branches, so that
+          // the exponentials of many keys are in flight
           uint64_t sum[4] = {0, 0, 0, 0};
+          auto two = [&](int j) {                            // keys j, j + 1
+            float p0, p1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, ref2), p0, p1);
+            const uint64_t p2 =
+                pack_f32x2(__float_as_uint(exp2_fast(p0)), __float_as_uint(exp2_fast(p1)));
+            sum[(j >> 1) & 3] = add_f32x2(sum[(j >> 1) & 3], p2);
+            unpack_f32x2(p2, p0, p1);
+            x[j >> 1] = pack_bf16(p0, p1);
+            return p2;
+          };
+          if (heavy == 0) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            float e[16];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const int n = 16 * g + j;
-              unpack_f32x2(fma_f32x2(pack_f32x2(x[n], x[n + 1]), scale2, ref2), e[j], e[j + 1]);
-              e[j] = exp2_fast(e[j]);
-              e[j + 1] = exp2_fast(e[j + 1]);
-              sum[(j >> 1) & 3] =
-                  add_f32x2(sum[(j >> 1) & 3],
-                            pack_f32x2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
-              x[n >> 1] = pack_bf16(e[j], e[j + 1]);
+            for (int j = 0; j < kTile; j += 2) {
+              two(j);
+              if (j == kTile / 2 - 2) tmem_st_32x32b_x32(sS, x);
             }
-            if ((heavy >> g) & 1u) {
-              uint32_t rest[8];
+          } else {
+            const uint64_t minus1 = pack_f32x2(0xbf800000u, 0xbf800000u);
+            uint32_t rest[kTile / 2];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t u = x[8 * g + j];
-                rest[j] = pack_bf16(e[2 * j] - __uint_as_float(u << 16),
-                                    e[2 * j + 1] - __uint_as_float(u & 0xffff0000u));
-              }
-              tmem_st_32x32b_x8(sS + 64 + 8 * g, rest);
+            for (int j = 0; j < kTile; j += 2) {
+              const uint64_t p2 = two(j);
+              const uint32_t u = x[j >> 1];
+              float r0, r1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(u << 16, u & 0xffff0000u), minus1, p2), r0, r1);
+              rest[j >> 1] = pack_bf16(r0, r1);
             }
-            if (g == 3) tmem_st_32x32b_x32(sS, x);
+            tmem_st_32x32b_x32(sS, x);
+            tmem_st_32x32b_x32(sS + 64, rest);
+            tmem_st_32x32b_x32(sS + 96, rest + 32);
           }
           tmem_st_32x32b_x32(sS + 32, x + 32);
           {
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileSpan t = tile_span(p, it.tile0 + i);
             // rare: value rows that were cleared although some rows see them
             const int pos_v = ring0 + ring_v(pair, it.ntiles, i);
-            ok = warp_wait_count(&b->mended[st], n_mended, b, a.dev_status);
+            ok = warp_wait_count(&b->mended[st], n_mended, b);
             if (!ok) break;
             uint32_t left = 0;
             for (int n = -1;;) {
@@ -859,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (n_st > 0) {
-        ok = warp_wait(&b->s_full[st], ph_s, b, a.dev_status);      // O is complete
+        ok = warp_wait(&b->s_full[st], ph_s, b);      // O is complete
         if (!ok) break;
         ph_s ^= 1;
         tc_fence_after();
@@ -877,12 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&b->ml_full);
-          ok = warp_wait(&b->ml_empty, ph_ml, b, a.dev_status);
+          ok = warp_wait(&b->ml_empty, ph_ml, b);
           if (!ok) break;
           ph_ml ^= 1;
           continue;
         }
-        ok = warp_wait(&b->ml_full, ph_ml, b, a.dev_status);
+        ok = warp_wait(&b->ml_full, ph_ml, b);
         if (!ok) break;
         ph_ml ^= 1;
         tc_fence_after();
@@ -954,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->wg[st]);
-      ok = warp_wait(&b->wg[st], ph_wg, b, a.dev_status);
+      ok = warp_wait(&b->wg[st], ph_wg, b);
       if (!ok) break;
       ph_wg ^= 1;
       if (row == 0) {
@@ -963,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->wg[st]);
-      ok = warp_wait(&b->wg[st], ph_wg, b, a.dev_status);
+      ok = warp_wait(&b->wg[st], ph_wg, b);
       if (!ok) break;
       ph_wg ^= 1;
       if (!b->last[st]) continue;
@@ -985,6 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc<512>(tmem);
+  if (threadIdx.x == 0 && b->abort_flag != 0)
+    atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_DEVICE_TIMEOUT));
 }
 
 cudaError_t encode_pool(CUtensorMap* map, const AttnArgs& a, int kv, int rows) {

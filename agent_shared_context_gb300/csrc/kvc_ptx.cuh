@@ -83,23 +83,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
-// The same for waits that hand over between warps within a microsecond: reading
-// the timer costs several hundred cycles, so it is read (and *abort looked at)
-// every 4,096 polls only.
-__device__ __forceinline__ bool mbar_wait_polling(uint64_t* bar, uint32_t parity,
-                                                  uint64_t limit_ns, const volatile int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 4095u) == 0u) {
-      if (*abort) return false;
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > limit_ns) return false;
-    }
-  }
-}
-
 // ------------------------------------------------------------------ proxies
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -165,19 +165,27 @@ Ptr = Union[None, int, "torch.Tensor"]  # noqa: F821
 
 
 def _addr(x: Ptr) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return int(x.data_ptr())
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_raw_stream = None      # (device of the thread, its current stream) getters, once CUDA is up
 
 
 def _stream(stream) -> Optional[int]:
+    """The handle of a stream, or of torch's current one.  A small call spends most
+    of its time on the host: building a torch Stream object would cost 3 us of it."""
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:
+            device, current = _raw_stream
+            return current(device())
         import torch
         if not torch.cuda.is_available():
             return None
-        return int(torch.cuda.current_stream().cuda_stream)
+        handle = int(torch.cuda.current_stream().cuda_stream)
+        if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+            _raw_stream = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        return handle
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -193,10 +201,10 @@ def cache_view(t: Ptr, strides: Optional[Sequence[int]] = None) -> kvc_cache_vie
     if isinstance(t, int):
         s = tuple(int(v) for v in strides)
         return kvc_cache_view(t, *s)
-    if t.dim() != 5 or t.stride(-1) != 1:
-        raise ValueError("cache tensors are [R, L, H, T, d] with a contiguous last dimension")
     st = t.stride()
-    return kvc_cache_view(int(t.data_ptr()), st[0], st[1], st[2], st[3])
+    if len(st) != 5 or st[4] != 1:
+        raise ValueError("cache tensors are [R, L, H, T, d] with a contiguous last dimension")
+    return kvc_cache_view(t.data_ptr(), st[0], st[1], st[2], st[3])
 
 
 class Segments:
@@ -264,7 +272,7 @@ def _done(st: int, where: str, check: bool) -> int:
 def _nbytes(t: Ptr) -> int:
     if t is None or isinstance(t, int):
         return 0
-    return int(t.numel() * t.element_size())
+    return t.numel() * t.element_size()
 
 
 # --------------------------------------------------------------- entry points
