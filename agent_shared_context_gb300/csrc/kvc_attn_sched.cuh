@@ -382,7 +382,7 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
 #pragma unroll 4
     for (int p = 0; p < it.nparts; ++p)
       M = fmaxf(M, __ldcg(part(p) + slot_rows * d + row0 + row));
-    constexpr int kC = 8;
+    constexpr int kC = 4;
 #pragma unroll 1
     for (int c0 = tid / span; c0 < d4; c0 += kC * step) {
       float4 acc[kC];

@@ -42,7 +42,7 @@
 // The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
 // 2^-8 average out over many keys of like weight but not where few carry a
 // row, so the remainder P - bf16(P) is multiplied too, in the steps of 16 keys
-// in which some row has a key with more than 1/5 of its sum so far (1/16 in
+// in which some row has a key with more than 1/8 of its sum so far (1/16 in
 // single mode, which waits for memory anyway): few steps of a long context.  S
 // leaves room for it in TMEM, beside P.
 //
@@ -68,13 +68,14 @@ constexpr int kRegsSoftmax = 208;          // 256 threads x 208 + 128 x 88 = 384
 constexpr int kRegsOther = 88;
 constexpr int kRowsM = 128;                // rows of a stream (MMA M)
 constexpr int kTile = 128;                 // keys of a tile
+constexpr int kHalf = kTile / 2;           // keys of a step of a stream
 constexpr int kSubBytes = kTile * 128;     // 128 rows x 64 bf16
 constexpr int kSlotRows = 256;             // rows of a partial result
 constexpr int kMaxCtas = 160;
 constexpr int kItems = 4;                  // depth of the item ring
 constexpr int kNoPage = INT32_MIN;         // no key there: read as zeros
 constexpr float kLag = 8.0f;               // log2 by which m may lag behind
-constexpr float kHeavyPair = 0.2f;         // share of a row's sum that makes a key heavy
+constexpr float kHeavyPair = 0.125f;       // share of a row's sum that makes a key heavy
 constexpr float kHeavySingle = 0.0625f;
 
 template <int D>
@@ -110,7 +111,7 @@ struct ItemSlot {
 
 // What a stream's softmax tells its MMA warp along with P.
 struct alignas(8) Told {
-  uint32_t heavy;          // steps of 16 keys with a remainder, a byte per warp
+  uint32_t heavy;          // MMA steps of 16 keys with a remainder, a byte per warp
   int32_t o_init;          // O holds something before the first P V
 };
 
@@ -118,8 +119,7 @@ template <int NS>
 struct Bars {
   uint64_t kv_full[NS], kv_raw[NS], kv_empty[NS];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2];
-  uint64_t turn[2];                // pair mode: whose MMAs are issued next
+  uint64_t s_full[2][2], p_full[2][2];   // [stream][half of the tile's keys]
   uint64_t o_seen[2];              // the stream's warps know that an item's O is complete
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t ml_full, ml_empty;      // stream 1's row statistics for stream 0
@@ -128,7 +128,7 @@ struct Bars {
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t last[2];
-  Told told[2];
+  Told told[2][2];
   int32_t mended[2];               // value tiles of each stream that were mended so far
   uint32_t poison[NS][4];          // cleared value rows that some rows of the item see
   float ml[kRowsM][2];
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs p) {
   using C = Cfg<D>;
   constexpr int NS = C::kSlots;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsM, kTile);
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsM, kHalf);
   constexpr uint32_t kIdescO = idesc_bf16_f32(kRowsM, D) | kIdescBMnMajor;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<NS> bars_mem;
@@ -291,10 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&b->q_full, 1);
     mbar_init(&b->q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->p_full[i], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&b->s_full[i][h], 1);
+        mbar_init(&b->p_full[i][h], 4);
+      }
       mbar_init(&b->o_seen[i], 4);
-      mbar_init(&b->turn[i], 1);
       mbar_init(&b->wg[i], 4);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -473,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc_k = desc_kmajor_sw128(smem_u32(kv_smem));
     const uint64_t desc_v = desc_mnmajor_sw128(smem_u32(kv_smem), kSubBytes);
     uint32_t ph_p = 0, ph_o = 0;
-    uint32_t ph_turn = st == 0 ? 1 : 0;            // stream 0 begins
     bool ended = false;                            // an item's O may not be seen yet
     bool ok = true;
     for (int n_items = 0; ok; ++n_items) {
@@ -523,54 +523,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph_o ^= 1;
       }
       ended = true;
-      // per turn: O += P V of the tile before, then S of tile i
+      // For each half of the keys: O += P V of the tile before, then S of tile i, so
+      // that a half's scores are made while the other half's are exponentiated.
 #pragma unroll 1
       for (int i = first;; i += step) {
         const bool pv = i > first, more = i < n;
         const int v_at = ring0 + ring_v(pair, n, i - step), k_at = ring0 + ring_k(pair, i);
-        ok = (!pv || own(v_at)) && (!more || own(k_at)) &&
-             (!pv || warp_wait(&b->p_full[st], ph_p, b));
-        // In pair mode the streams take turns: were their MMAs to mix, both would get
-        // their scores late and together, and the tensor core would idle meanwhile.
-        if (ok && pair) {
-          ok = warp_wait(&b->turn[st], ph_turn, b);
-          ph_turn ^= 1;
-        }
+        ok = (!pv || own(v_at)) && (!more || own(k_at));
         if (!ok) break;
-        tc_fence_after();
-        if (pv) {
-          ph_p ^= 1;
-          const volatile Told* told = &b->told[st];
-          const uint32_t heavy = told->heavy;
-          const bool acc = i > first + step || told->o_init != 0;
-          const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ts_warp(dO, dS + k * 8, dv + k * (2048 >> 4), kIdescO, acc || k > 0);
-          if (heavy != 0) {
-            // the remainders of P, for the warps that have one in the step
+        const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
+        const uint64_t dk = desc_k + static_cast<uint64_t>(k_at % NS * (C::kSlotBytes >> 4));
 #pragma unroll 1
-            for (int k = 0; k < kTile / 16; ++k) {
-              const uint32_t who = (heavy >> k) & 0x01010101u;
-              if (who == 0) continue;
-              const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
-                                       ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
-              mma_bf16_ts_warp_lanes(dO, dS + 64 + k * 8, dv + k * (2048 >> 4), kIdescO, off);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t tS_h = dS + h * kHalf;
+          if (pv) {
+            ok = warp_wait(&b->p_full[st][h], ph_p, b);
+            if (!ok) break;
+            tc_fence_after();
+            const volatile Told* told = &b->told[st][h];
+            const uint32_t heavy = told->heavy;
+            const bool acc = i > first + step || h > 0 || told->o_init != 0;
+            const uint64_t dvh = dv + h * (kHalf * 128 >> 4);
+#pragma unroll
+            for (int k = 0; k < kHalf / 16; ++k)
+              mma_bf16_ts_warp(dO, tS_h + k * 8, dvh + k * (2048 >> 4), kIdescO, acc || k > 0);
+            if (heavy != 0) {
+              // the remainders of P, for the warps that have one in the step
+#pragma unroll 1
+              for (int k = 0; k < kHalf / 16; ++k) {
+                const uint32_t who = (heavy >> k) & 0x01010101u;
+                if (who == 0) continue;
+                const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
+                                         ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
+                mma_bf16_ts_warp_lanes(dO, tS_h + kHalf / 2 + k * 8, dvh + k * (2048 >> 4), kIdescO,
+                                       off);
+              }
             }
           }
-        }
-        if (more) {
-          const uint64_t dk = desc_k + static_cast<uint64_t>(k_at % NS * (C::kSlotBytes >> 4));
+          if (more) {
+            const uint64_t dkh = dk + h * (kHalf * 128 >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
-            mma_bf16_ss_warp(dS, dq + off, dk + off, kIdescS, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
+              mma_bf16_ss_warp(tS_h, dq + off, dkh + off, kIdescS, k > 0);
+            }
           }
+          mma_commit_warp(&b->s_full[st][h]);
         }
-        mma_commit_warp(&b->s_full[st]);
-        if (pair && lane == 0) mbar_arrive(&b->turn[st ^ 1]);
-        __syncwarp();
-        if (pv) mma_commit_warp(&b->kv_empty[v_at % NS]);
+        if (!ok) break;
+        if (pv) {
+          ph_p ^= 1;
+          mma_commit_warp(&b->kv_empty[v_at % NS]);
+        }
         if (!more) break;
         mma_commit_warp(&b->kv_empty[k_at % NS]);
         if (i + step >= n) mma_commit_warp(&b->q_empty);
@@ -702,51 +706,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
 
-      for (int k = 0; k < n_st; ++k) {
+      for (int kh = 0; kh < 2 * n_st; ++kh) {               // halves of the stream's tiles
+        const int k = kh >> 1, half = kh & 1;
         const int i = pair ? k : 2 * k + st;                // key tile of the item
-        ok = warp_wait(&b->s_full[st], ph_s, b);
+        ok = warp_wait(&b->s_full[st][half], ph_s, b);
         if (!ok) break;
-        ph_s ^= 1;
         const bool edge = it.tile0 + i < edge_lo || it.tile0 + i >= edge_hi;
-        n_mended += edge;
+        n_mended += edge & (half == 0);
+        const uint32_t sH = sS + half * kHalf;
         if (busy) {
           tc_fence_after();
-          uint32_t x[kTile];
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) tmem_ld_32x32b_x32(sS + c, x + c);
+          // O may be touched once the product of the half before is in it: that half's next
+          // scores (or the end of the item) are signalled after it
+          auto settle = [&]() {
+            const bool there = warp_wait(&b->s_full[st][half ^ 1], ph_s ^ (half ? 1u : 0u), b);
+            tc_fence_after();
+            return there;
+          };
+          uint32_t x[kHalf];
+          tmem_ld_32x32b_x32(sH, x);
+          tmem_ld_32x32b_x32(sH + 32, x + 32);
           tmem_ld_wait();
           if (edge || p.ragged) {
             const TileSpan t = tile_span(p, it.tile0 + i);
-            const int lo = tile_col(p, t, key_lo);
-            const int hi = min(tile_col(p, t, key_hi), p.has_holes ? kTile : t.cnt);
+            const int lo = tile_col(p, t, key_lo) - half * kHalf;
+            const int hi = min(tile_col(p, t, key_hi), p.has_holes ? kTile : t.cnt) - half * kHalf;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t keep =
-                  bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) & ~p.holes[c];
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t keep = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) &
+                                    ~(half == 0 ? p.holes[c] : p.holes[2 + c]);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (!((keep >> j) & 1u)) x[32 * c + j] = 0xff800000u;      // -inf
             }
           }
           auto sc = [&](int j) { return __uint_as_float(x[j]); };
-          float mx[8];                                       // of each 16 keys
+          float mx[4];                                       // of each 16 keys
 #pragma unroll
-          for (int g = 0; g < 8; ++g) mx[g] = max3(sc(16 * g), sc(16 * g + 1), sc(16 * g + 2));
+          for (int g = 0; g < 4; ++g) mx[g] = max3(sc(16 * g), sc(16 * g + 1), sc(16 * g + 2));
 #pragma unroll
           for (int j = 3; j < 15; j += 2)
 #pragma unroll
-            for (int g = 0; g < 8; ++g) mx[g] = max3(mx[g], sc(16 * g + j), sc(16 * g + j + 1));
+            for (int g = 0; g < 4; ++g) mx[g] = max3(mx[g], sc(16 * g + j), sc(16 * g + j + 1));
 #pragma unroll
-          for (int g = 0; g < 8; ++g) mx[g] = fmaxf(mx[g], sc(16 * g + 15));
-          const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
-                                 fmaxf(mx[6], mx[7])) *
-                            a.scale_log2;
+          for (int g = 0; g < 4; ++g) mx[g] = fmaxf(mx[g], sc(16 * g + 15));
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
           const bool raise = top > m + kLag || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, raise)) {
             const float f = raise ? exp2_fast(m - top) : 1.f;              // 0 from m = -inf
             if (raise) m = top;
             l *= f;
-            if (k > 0) {
+            if (kh > 0) {
+              ok = settle();
+              if (!ok) break;
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -768,77 +780,73 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float least = (pair ? kHeavyPair : kHeavySingle) * (l + p_top);
           if (__any_sync(0xffffffffu, valid && p_top > least)) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
+            for (int g = 0; g < 4; ++g)
               if (__any_sync(0xffffffffu,
                              valid && exp2_fast(fmaf(mx[g], a.scale_log2, -ref)) > least))
                 heavy |= 1u << g;
           }
           // P, and its remainder where it is wanted, in passes without branches, so that
           // the exponentials of many keys are in flight
-          uint64_t sum[4] = {0, 0, 0, 0};
+          uint64_t sum[2] = {0, 0};
           auto two = [&](int j) {                            // keys j, j + 1
             float p0, p1;
             unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, ref2), p0, p1);
             const uint64_t p2 =
                 pack_f32x2(__float_as_uint(exp2_fast(p0)), __float_as_uint(exp2_fast(p1)));
-            sum[(j >> 1) & 3] = add_f32x2(sum[(j >> 1) & 3], p2);
+            sum[(j >> 1) & 1] = add_f32x2(sum[(j >> 1) & 1], p2);
             unpack_f32x2(p2, p0, p1);
             x[j >> 1] = pack_bf16(p0, p1);
             return p2;
           };
           if (heavy == 0) {
 #pragma unroll
-            for (int j = 0; j < kTile; j += 2) {
-              two(j);
-              if (j == kTile / 2 - 2) tmem_st_32x32b_x32(sS, x);
-            }
+            for (int j = 0; j < kHalf; j += 2) two(j);
           } else {
             const uint64_t minus1 = pack_f32x2(0xbf800000u, 0xbf800000u);
-            uint32_t rest[kTile / 2];
+            uint32_t rest[kHalf / 2];
 #pragma unroll
-            for (int j = 0; j < kTile; j += 2) {
+            for (int j = 0; j < kHalf; j += 2) {
               const uint64_t p2 = two(j);
               const uint32_t u = x[j >> 1];
               float r0, r1;
               unpack_f32x2(fma_f32x2(pack_f32x2(u << 16, u & 0xffff0000u), minus1, p2), r0, r1);
               rest[j >> 1] = pack_bf16(r0, r1);
             }
-            tmem_st_32x32b_x32(sS, x);
-            tmem_st_32x32b_x32(sS + 64, rest);
-            tmem_st_32x32b_x32(sS + 96, rest + 32);
+            tmem_st_32x32b_x32(sH + kHalf / 2, rest);
           }
-          tmem_st_32x32b_x32(sS + 32, x + 32);
+          tmem_st_32x32b_x32(sH, x);
           {
             float s0, s1;
-            unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+            unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
           }
           if (lane == 0)
-            reinterpret_cast<volatile uint8_t*>(&b->told[st].heavy)[warp & 3] = heavy;
+            reinterpret_cast<volatile uint8_t*>(&b->told[st][half].heavy)[warp & 3] = heavy;
           tmem_st_wait();
 
           bool init = false;
           if (edge) {
-            const TileSpan t = tile_span(p, it.tile0 + i);
             // rare: value rows that were cleared although some rows see them
             const int pos_v = ring0 + ring_v(pair, it.ntiles, i);
             ok = warp_wait_count(&b->mended[st], n_mended, b);
             if (!ok) break;
-            uint32_t left = 0;
-            for (int n = -1;;) {
-              // the next set bit, in order
-              while (left == 0 && (n >> 5) < 3) {
-                n = ((n >> 5) + 1) << 5;
-                left = b->poison[pos_v % NS][n >> 5];
+            const uint32_t* bad = &b->poison[pos_v % NS][2 * half];
+            if ((bad[0] | bad[1]) != 0 && kh > 0) {
+              ok = settle();
+              if (!ok) break;
+            }
+#pragma unroll 1
+            for (int n = 0; n < kHalf; ++n) {
+              if (!((bad[n >> 5] >> (n & 31)) & 1u)) {
+                if ((bad[n >> 5] >> (n & 31)) == 0) n |= 31;      // none left in the word
+                continue;
               }
-              if (left == 0) break;
-              n = (n & ~31) + __ffs(left) - 1;
-              left &= left - 1;
-              const int tok = tile_tok(p, t, n), blk = fast_div(tok, p.page);
+              const TileSpan t = tile_span(p, it.tile0 + i);
+              const int tok = tile_tok(p, t, n + half * kHalf), blk = fast_div(tok, p.page);
               const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
-              const uint32_t two = tmem_ld_32x32b_x1(sS + (n >> 1));
+              const uint32_t two_p = tmem_ld_32x32b_x1(sH + (n >> 1));
               tmem_ld_wait();
-              const float pr = __uint_as_float((n & 1) ? two & 0xffff0000u : two << 16);
+              const float pr = __uint_as_float((n & 1) ? two_p & 0xffff0000u : two_p << 16);
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool[1].base) +
                                        page * a.pool[1].s_req + a.layer * a.pool[1].s_layer +
                                        it.h * a.pool[1].s_head +
@@ -850,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  const float old = k > 0 || init ? __uint_as_float(o[j]) : 0.f;
+                  const float old = kh > 0 || init ? __uint_as_float(o[j]) : 0.f;
                   const float add = pr == 0.f ? 0.f : pr * __bfloat162float(v[c + j]);
                   o[j] = __float_as_uint(old + add);
                 }
@@ -860,17 +868,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               init = true;
             }
           }
-          if (k == 0 && (warp & 3) == 0 && lane == 0) b->told[st].o_init = init ? 1 : 0;
+          if (kh == 0 && (warp & 3) == 0 && lane == 0) b->told[st][0].o_init = init ? 1 : 0;
           tc_fence_before();
         } else if (lane == 0) {
-          reinterpret_cast<volatile uint8_t*>(&b->told[st].heavy)[warp & 3] = 0;
+          reinterpret_cast<volatile uint8_t*>(&b->told[st][half].heavy)[warp & 3] = 0;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[st]);
+        if (lane == 0) mbar_arrive(&b->p_full[st][half]);
+        ph_s ^= half;                                        // both halves' phases are alike
       }
       if (!ok) break;
       if (n_st > 0) {
-        ok = warp_wait(&b->s_full[st], ph_s, b);      // O is complete
+        // O is complete
+        ok = warp_wait(&b->s_full[st][0], ph_s, b) && warp_wait(&b->s_full[st][1], ph_s, b);
         if (!ok) break;
         ph_s ^= 1;
         tc_fence_after();
