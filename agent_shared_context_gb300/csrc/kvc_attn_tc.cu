@@ -29,15 +29,15 @@
 //   warps 9, 11     issue stream 0's and 1's S = Q K^T (both K-major in shared
 //                   memory) and O += P V (P in TMEM, V as the MN-major operand
 //                   it is);
-//   warp 10         mends value tiles at the edge of sight (below).
+//   warp 10         only holds its place in its warpgroup.
 //
 // A key tile is 128 rows of a page, or as many whole pages (rounded up to 8
 // rows) as fit: pages of 8, 16, 32, 64 rows fill it, others leave holes that
 // are masked.  Where a tile is not in sight of all its rows the scores are
-// masked and warp 10 clears the value rows that no row sees, because 0 times
-// whatever the page holds there need not be 0.  A value row that some rows see
-// and others do not may hold an infinity or a NaN as well: it is cleared too,
-// and the rows that do see it add its products from memory.
+// masked, and the softmax warps look through the value rows that are not in
+// sight of all: 0 times an infinity or a NaN, which a page may hold there, is not
+// 0.  Where they find one they clear it, and if some rows do see it those add its
+// products from memory.
 //
 // The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
 // 2^-8 average out over many keys of like weight but not where few carry a
@@ -101,12 +101,13 @@ struct TcArgs {
   uint32_t holes[4];       // columns of a tile that never hold a key (pages < 128 rows)
   int32_t has_holes;
   int32_t ragged;          // some tiles hold fewer than 128 keys
+  int32_t out32;           // output rows are 32-byte aligned
 };
 
 struct ItemSlot {
   Item it;
   int32_t ring0;           // ring position of the item's first K tile
-  int32_t edge_lo, edge_hi;  // key tiles below and from which value rows need mending
+  int32_t edge_lo, edge_hi;  // key tiles below and from which not every row sees all keys
 };
 
 // What a stream's softmax tells its MMA warp along with P.
@@ -117,7 +118,7 @@ struct alignas(8) Told {
 
 template <int NS>
 struct Bars {
-  uint64_t kv_full[NS], kv_raw[NS], kv_empty[NS];
+  uint64_t kv_full[NS], kv_empty[NS];
   uint64_t q_full, q_empty;
   uint64_t s_full[2][2], p_full[2][2];   // [stream][half of the tile's keys]
   uint64_t o_seen[2];              // the stream's warps know that an item's O is complete
@@ -129,8 +130,8 @@ struct Bars {
   int32_t abort_flag;
   int32_t last[2];
   Told told[2][2];
-  int32_t mended[2];               // value tiles of each stream that were mended so far
-  uint32_t poison[NS][4];          // cleared value rows that some rows of the item see
+  int32_t landed[2];               // value tiles that each stream's MMA warp has seen land
+  uint32_t poison[NS][4];          // value rows with an infinity or NaN that some rows see
   float ml[kRowsM][2];
   ItemSlot items[kItems];
   Shared sched;
@@ -254,8 +255,7 @@ __device__ __forceinline__ Sight sight(const AttnArgs& a, int kv, int pos0, int 
   return s;
 }
 
-// Key tiles that not every row sees whole: below *lo and from *hi on.  Their
-// value rows are mended before the product.
+// Key tiles that not every row sees whole: below *lo and from *hi on.
 __device__ __forceinline__ void edges(const SchedArgs& a, const Sight& s, int* lo, int* hi) {
   *lo = s.all_lo > 0 ? tile_of(a, s.all_lo - 1) + 1 : 0;
   *hi = s.all_hi > 0 ? tile_of(a, s.all_hi) : 0;
@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&b->kv_full[i], 1);
-      mbar_init(&b->kv_raw[i], 1);
       mbar_init(&b->kv_empty[i], 2);       // one MMA warp for each stream
     }
     mbar_init(&b->q_full, 1);
@@ -300,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&b->item_full[i], 1);
-      mbar_init(&b->item_empty[i], 11);    // 8 softmax, 2 MMA warps and the mending one
+      mbar_init(&b->item_empty[i], 10);    // 8 softmax and 2 MMA warps
     }
     mbar_init(&b->ml_full, 4);
     mbar_init(&b->ml_empty, 4);
     mbar_init(&b->drain[0], 1);
     mbar_init(&b->drain[1], 1);
     b->abort_flag = 0;
-    b->mended[0] = b->mended[1] = 0;
+    b->landed[0] = b->landed[1] = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -342,8 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;                                    // ring % NS
     uint32_t wrap = 1;                            // parity of kv_empty[s] to wait for
     bool ok = true;
-    uint32_t raw_phase = 0;                       // bit i: parity of kv_raw[i]'s next phase
-    uint32_t raw_open = 0;                        // bit i: slot i's last load went to kv_raw
     const int boxes = p.pages_tile * C::kSub;
     const int my_page = lane / C::kSub, my_sub = lane - my_page * C::kSub;
     const uint32_t tile_bytes = static_cast<uint32_t>(p.pages_tile * p.page_rows) * 128 * C::kSub;
@@ -406,11 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pos = 0; pos < 2 * n; ++pos) {
         // the order in which the MMAs take them: ring_k, ring_v
         const bool is_v = pos == 2 * n - 1 || (pair ? (pos & 1) : pos >= 2 && !(pos & 1));
-        bool mend = false;
         int use, row;
         if (is_v) {
-          const int tile = it.tile0 + i_v;
-          mend = tile < edge_lo || tile >= edge_hi;
           use = i_v + 1 == i_k ? page : page_before;
           ++i_v;
           row = row_v;
@@ -432,16 +426,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           row = row_k;
           row_k = row + kTile == row_end ? 0 : row + kTile;
         }
-        uint64_t* bar = mend ? &b->kv_raw[s] : &b->kv_full[s];
+        uint64_t* bar = &b->kv_full[s];
         ok = warp_wait(&b->kv_empty[s], wrap, b);
         if (!ok) break;
+        if (is_v && lane < 4) b->poison[s][lane] = 0;
+        __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
         __syncwarp();
         if (lane < boxes)
           tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64, row,
                       it.h, a.layer, use);
-        raw_open = mend ? raw_open | 1u << s : raw_open & ~(1u << s);
-        raw_phase ^= static_cast<uint32_t>(mend) << s;
         ++ring;
         if (++s == NS) {
           s = 0;
@@ -453,13 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad_page) atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
     if (!ok) {
       // the copies in flight write to this CTA's shared memory: let them land
-      for (int i = ring - 1; i >= 0 && i >= ring - NS; --i) {
-        const int s = i % NS;
-        if ((raw_open >> s) & 1)
-          mbar_wait_bounded(&b->kv_raw[s], ((raw_phase >> s) & 1) ^ 1, kWaitLimitNs);
-        else
-          mbar_wait_bounded(&b->kv_full[s], (i / NS) & 1, kWaitLimitNs);
-      }
+      for (int i = ring - 1; i >= 0 && i >= ring - NS; --i)
+        mbar_wait_bounded(&b->kv_full[i % NS], (i / NS) & 1, kWaitLimitNs);
       if (n_items > 0) mbar_wait_bounded(&b->q_full, (n_items - 1) & 1, kWaitLimitNs);
     }
   } else if (warp == 9 || warp == 11) {
@@ -529,7 +518,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = first;; i += step) {
         const bool pv = i > first, more = i < n;
         const int v_at = ring0 + ring_v(pair, n, i - step), k_at = ring0 + ring_k(pair, i);
-        ok = (!pv || own(v_at)) && (!more || own(k_at));
+        if (pv) {
+          ok = own(v_at);
+          if (!ok) break;
+          if (lane == 0) {
+            volatile int32_t* landed = &b->landed[st];
+            *landed = *landed + 1;
+          }
+        }
+        if (more) ok = own(k_at);
         if (!ok) break;
         const uint64_t dv = desc_v + static_cast<uint64_t>(v_at % NS * (C::kSlotBytes >> 4));
         const uint64_t dk = desc_k + static_cast<uint64_t>(k_at % NS * (C::kSlotBytes >> 4));
@@ -586,87 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(&b->drain[st], 0, kWaitLimitNs);
       __syncwarp();
     }
-  } else if (warp == 10) {
-    // ------------------------------------------------- value tiles at an edge
-    uint32_t raw_phase = 0;
-    bool ok = true;
-    for (int n_items = 0; ok; ++n_items) {
-      const int slot = n_items % kItems;
-      ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b);
-      if (!ok) break;
-      const Item it = b->items[slot].it;
-      const int ring0 = b->items[slot].ring0;
-      const int edge_lo = b->items[slot].edge_lo, edge_hi = b->items[slot].edge_hi;
-      __syncwarp();
-      if (it.ntiles == 0) break;
-      if (lane == 0) mbar_arrive(&b->item_empty[slot]);
-      const bool pair = it.nt > p.tok_tile;
-      const Sight see = sight(a, it.kv, it.pos0, it.nt);
-      for (int i = 0; i < it.ntiles && ok; ++i) {
-        if (it.tile0 + i >= edge_lo && it.tile0 + i < edge_hi) {
-          i = min(it.ntiles, edge_hi - it.tile0) - 1;       // on to the upper edge
-          continue;
-        }
-        const TileSpan t = tile_span(p, it.tile0 + i);
-        const int s = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
-        ok = warp_wait(&b->kv_raw[s], (raw_phase >> s) & 1, b);
-        if (!ok) break;
-        raw_phase ^= 1u << s;
-        const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
-        const int c1 = tile_col(p, t, see.all_lo), c2 = tile_col(p, t, see.all_hi);
-        uint8_t* rows = kv_smem + s * C::kSlotBytes;
-        if (lane < 4) b->poison[s][lane] = 0;
-        // kLanes lanes hold a row, 16 bytes each, kPer rows at a time
-        constexpr int kLanes = 8 * C::kSub, kPer = 32 / kLanes;
-        const int my_row = lane / kLanes;
-        uint8_t* mine = rows + (lane % kLanes) / 8 * kSubBytes + lane % 8 * 16;
-        // rows that no row sees: [0, c0), [c3, 128)
-#pragma unroll 1
-        for (int n = my_row; n < kTile; n += kPer)
-          if (n < c0 || n >= c3)
-            *reinterpret_cast<uint4*>(mine + n * 128) = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-        // rows that some rows see: [c0, c1), [c2, c3)
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          const int lo = part == 0 ? c0 : max(max(c0, c1), c2), hi = part == 0 ? min(c1, c3) : c3;
-          constexpr int kU = 4;
-#pragma unroll 1
-          for (int n0 = lo; n0 < hi; n0 += kPer * kU) {
-            uint4 v[kU];
-#pragma unroll
-            for (int j = 0; j < kU; ++j) {
-              const int n = n0 + j * kPer + my_row;
-              v[j] = n < hi ? *reinterpret_cast<const uint4*>(mine + n * 128)
-                            : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int j = 0; j < kU; ++j) {
-              auto odd = [](uint32_t u) {                    // an exponent of all ones
-                return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-              };
-              const uint32_t who = __ballot_sync(
-                  0xffffffffu, odd(v[j].x) || odd(v[j].y) || odd(v[j].z) || odd(v[j].w));
-              if (who == 0) continue;
-              const int n = n0 + j * kPer + my_row;
-              if ((who >> (my_row * kLanes)) & bits_below(kLanes)) {
-                *reinterpret_cast<uint4*>(mine + n * 128) = make_uint4(0, 0, 0, 0);
-                if (lane % kLanes == 0) atomicOr(&b->poison[s][n >> 5], 1u << (n & 31));
-              }
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __threadfence_block();
-        __syncwarp();
-        if (lane == 0) {
-          volatile int32_t* mended = b->mended;
-          if (pair || (i & 1) == 0) mended[0] = mended[0] + 1;
-          if (pair || (i & 1) == 1) mended[1] = mended[1] + 1;
-          mbar_arrive(&b->kv_full[s]);
-        }
-      }
-    }
   }
   } else {
     // -------------------------------------------------------------- softmax
@@ -678,12 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_tok = row / a.G, row_g = row - row_tok * a.G;
     const bool row_in_tile = row_tok < p.tok_tile;
     uint32_t ph_s = 0, ph_wg = 0, ph_ml = 0;
-    int32_t n_mended = 0;                         // value tiles of the stream at an edge so far
+    int32_t n_tiles = 0;                          // tiles of the stream in earlier items
     int32_t* counters = static_cast<int32_t*>(a.workspace);
     float* slots =
         reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
     const size_t slot_n = slot_floats(kSlotRows, D);
     bool ok = true;
+    // the four warps of the stream meet
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->wg[st]);
+      const bool met = warp_wait(&b->wg[st], ph_wg, b);
+      ph_wg ^= 1;
+      return met;
+    };
 
     for (int n_items = 0; ok; ++n_items) {
       const int slot = n_items % kItems;
@@ -709,11 +633,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kh = 0; kh < 2 * n_st; ++kh) {               // halves of the stream's tiles
         const int k = kh >> 1, half = kh & 1;
         const int i = pair ? k : 2 * k + st;                // key tile of the item
+        const bool edge = it.tile0 + i < edge_lo || it.tile0 + i >= edge_hi;
+        const uint32_t sH = sS + half * kHalf;
+        const uint32_t* bad = nullptr;                      // value rows that are added from memory
+        if (edge) {
+          const int slot_v = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
+          ok = warp_wait_count(&b->landed[st], n_tiles + k + 1, b);
+          if (!ok) break;
+          const TileSpan t = tile_span(p, it.tile0 + i);
+          const Sight see = sight(a, it.kv, it.pos0, it.nt);
+          const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
+          const int c1 = tile_col(p, t, see.all_lo), c2 = tile_col(p, t, see.all_hi);
+          uint8_t* rows = kv_smem + slot_v * C::kSlotBytes + half * kHalf * 128;
+          // 16 bytes at a time, neighbouring threads neighbouring bytes
+          auto at = [&](int j, int* n) {
+            const int u = row + 128 * j;
+            *n = half * kHalf + ((u >> 3) & (kHalf - 1));
+            return reinterpret_cast<uint4*>(rows + (u / (8 * kHalf)) * kSubBytes +
+                                            ((u >> 3) & (kHalf - 1)) * 128 + (u & 7) * 16);
+          };
+          auto odd = [](uint32_t u) {                       // an exponent of all ones
+            return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+          };
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            int n;
+            uint4* q = at(j, &n);
+            if (n >= c1 && n < c2) continue;
+            const uint4 v = *q;
+            if (!(odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w))) continue;
+            if (n >= c0 && n < c3) {
+              atomicOr(&b->poison[slot_v][n >> 5], 1u << (n & 31));
+            } else {
+              *q = make_uint4(0, 0, 0, 0);                  // no row sees it
+              fence_proxy_async_smem();
+            }
+          }
+          ok = meet();
+          if (!ok) break;
+          bad = &b->poison[slot_v][2 * half];
+          if ((bad[0] | bad[1]) != 0) {
+#pragma unroll 1
+            for (int j = 0; j < D / 16; ++j) {
+              int n;
+              uint4* q = at(j, &n);
+              if ((bad[(n >> 5) & 1] >> (n & 31)) & 1u) *q = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            ok = meet();
+            if (!ok) break;
+          } else {
+            bad = nullptr;
+          }
+        }
         ok = warp_wait(&b->s_full[st][half], ph_s, b);
         if (!ok) break;
-        const bool edge = it.tile0 + i < edge_lo || it.tile0 + i >= edge_hi;
-        n_mended += edge & (half == 0);
-        const uint32_t sH = sS + half * kHalf;
         if (busy) {
           tc_fence_after();
           // O may be touched once the product of the half before is in it: that half's next
@@ -825,13 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
 
           bool init = false;
-          if (edge) {
-            // rare: value rows that were cleared although some rows see them
-            const int pos_v = ring0 + ring_v(pair, it.ntiles, i);
-            ok = warp_wait_count(&b->mended[st], n_mended, b);
-            if (!ok) break;
-            const uint32_t* bad = &b->poison[pos_v % NS][2 * half];
-            if ((bad[0] | bad[1]) != 0 && kh > 0) {
+          if (bad != nullptr) {
+            if (kh > 0) {
               ok = settle();
               if (!ok) break;
             }
@@ -878,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph_s ^= half;                                        // both halves' phases are alike
       }
       if (!ok) break;
+      n_tiles += n_st;
       if (n_st > 0) {
         // O is complete
         ok = warp_wait(&b->s_full[st][0], ph_s, b) && warp_wait(&b->s_full[st][1], ph_s, b);
@@ -941,15 +911,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (valid && whole_item) {
+            uint32_t u[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 u;
-              const float* f = reinterpret_cast<const float*>(o + j);
-              u.x = pack_bf16(l == 0.f ? 0.f : f[0] * inv, l == 0.f ? 0.f : f[1] * inv);
-              u.y = pack_bf16(l == 0.f ? 0.f : f[2] * inv, l == 0.f ? 0.f : f[3] * inv);
-              u.z = pack_bf16(l == 0.f ? 0.f : f[4] * inv, l == 0.f ? 0.f : f[5] * inv);
-              u.w = pack_bf16(l == 0.f ? 0.f : f[6] * inv, l == 0.f ? 0.f : f[7] * inv);
-              *reinterpret_cast<uint4*>(out + c + j) = u;
+            for (int j = 0; j < 16; ++j)
+              u[j] = l == 0.f ? 0u
+                              : pack_bf16(__uint_as_float(o[2 * j]) * inv,
+                                          __uint_as_float(o[2 * j + 1]) * inv);
+            if (p.out32) {                         // whole sectors, half the requests
+              st_global_32(out + c, u);
+              st_global_32(out + c + 16, u + 8);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<uint4*>(out + c + 2 * j) =
+                    make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
             }
           } else if (valid) {
 #pragma unroll
@@ -973,20 +948,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // a divided item: join the parts if all others have left theirs
       __threadfence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->wg[st]);
-      ok = warp_wait(&b->wg[st], ph_wg, b);
+      ok = meet();
       if (!ok) break;
-      ph_wg ^= 1;
       if (row == 0) {
         __threadfence();
         b->last[st] = atomicAdd(counters + 2 * it.cta0 + st, 1) == it.nparts - 1;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->wg[st]);
-      ok = warp_wait(&b->wg[st], ph_wg, b);
+      ok = meet();
       if (!ok) break;
-      ph_wg ^= 1;
       if (!b->last[st]) continue;
       __threadfence();
       if (row == 0) counters[2 * it.cta0 + st] = 0;
@@ -1054,6 +1023,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   s.group_tiles = a.B < kTile ? 1 : (a.B + kTile - 1) / kTile;
   s.tile = make_fastdiv(a.B < kTile ? group : kTile);
   s.even = s.group_tiles == 1 || a.B % kTile == 0;
+  p.out32 = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) && (a.o_tok * 2) % 32 == 0 &&
+            (a.o_head * 2) % 32 == 0;
   p.ragged = p.has_holes || (a.B > kTile && a.B % kTile != 0);
   p.page = make_fastdiv(a.B);
   p.rows = make_fastdiv(p.page_rows);
