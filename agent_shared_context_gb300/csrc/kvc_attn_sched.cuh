@@ -4,14 +4,16 @@
 // The lengths of the requests live on the device, so the host cannot size the
 // work.  A *tile* is a fixed run of key rows (kTile of them at most), an *item*
 // is one (request, KV head, run of query tokens) and costs as many units as it
-// has key tiles in sight.  The units of all items, in the order request, head,
+// has key tiles in sight, and some for itself.  The units of all items, in the order request, head,
 // query run, are cut into equal shares, one per CTA of a persistent grid: a
 // single long decode, a batch of ragged ones and a dense prefill all fill the
-// GPU, with no work list to build first.  Every CTA adds the units up for
-// itself (R lengths from L2) and walks its share.  An item that spans several
-// shares leaves un-normalised partial rows (O, m, l) in the workspace; the CTA
-// that arrives last at the item's counter joins them in the order of their
-// key tiles, so the result does not depend on who was last.
+// GPU, with no work list to build first.  An item's beginning and end cost as
+// much as some tiles; it counts that many units more, before its first tile.
+// Every CTA adds the units up for itself (R lengths from L2) and walks its
+// share.  An item that spans several shares leaves un-normalised partial rows
+// (O, m, l) in the workspace; the CTA that arrives last at the item's counter
+// joins them in the order of their key tiles, so the result does not depend on
+// who was last.
 #pragma once
 
 #include <cstdint>
@@ -51,6 +53,7 @@ struct SchedArgs {
   FastDiv group;            // key tokens of a tile group (a page or several, below)
   FastDiv tile;             // key tokens per tile inside a group
   int32_t group_tiles;      // tiles per group
+  int32_t overhead;         // units of an item besides its tiles
   int32_t even;             // tile t holds the tokens [t tile, (t + 1) tile)
 };
 
@@ -95,7 +98,7 @@ __device__ __forceinline__ void item_tiles(const SchedArgs& a, const Request& q,
 __device__ __forceinline__ int item_units(const SchedArgs& a, const Request& q, int i) {
   int lo, hi;
   item_tiles(a, q, i * a.item.d, min(q.nq, (i + 1) * a.item.d), &lo, &hi);
-  return hi - lo;
+  return hi - lo + a.overhead;
 }
 
 __device__ __forceinline__ int n_items(const SchedArgs& a, const Request& q) {
@@ -135,7 +138,8 @@ static __device__ __noinline__ int64_t first_units(const SchedArgs& a, const Req
     const int64_t last = item_units(a, q, n - 1);      // the last may be shorter than an item
     if (!a.causal) return last * n;
     if (q.pos0 >= 0)
-      return last + floor_sum(n - 1, a.tile.d, a.item.d, q.pos0 + a.item.d + a.tile.d - 1);
+      return last + static_cast<int64_t>(n - 1) * a.overhead +
+             floor_sum(n - 1, a.tile.d, a.item.d, q.pos0 + a.item.d + a.tile.d - 1);
   }
   int64_t u = 0;
   for (int i = 0; i < n; ++i) u += item_units(a, q, i);
@@ -202,7 +206,9 @@ struct Walker {
         const int t0 = i * a.item.d, t1 = min(q.nq, t0 + a.item.d);
         int lo, hi;
         item_tiles(a, q, t0, t1, &lo, &hi);
-        const int64_t end = item_u0 + (hi - lo);
+        const int64_t first = item_u0 + a.overhead, end = first + (hi - lo);
+        if (u < first) u = first < u1 ? first : u1;
+        if (u >= u1) return false;
         if (u < end) {
           const int64_t stop = end < u1 ? end : u1;
           out->r = r;
@@ -212,10 +218,10 @@ struct Walker {
           out->q0 = q.q0 + t0;
           out->kv = q.kv;
           out->pos0 = q.pos0 + t0;
-          out->tile0 = lo + static_cast<int>(u - item_u0);
+          out->tile0 = lo + static_cast<int>(u - first);
           out->ntiles = static_cast<int>(stop - u);
           const int me = blockIdx.x;
-          const int c0 = u == item_u0 ? me : sh.owner(item_u0);
+          const int c0 = u == first ? me : sh.owner(first);
           out->cta0 = c0;
           out->part = me - c0;
           out->nparts = (end <= u1 ? me : sh.owner(end - 1)) - c0 + 1;
@@ -251,7 +257,7 @@ __device__ __forceinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_
   if (lane == 31) sh->warp_sum[warp] = v;
   __syncthreads();
   int64_t before = 0, all = 0;
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < THREADS / 32; ++w) {
     const int64_t x = sh->warp_sum[w];
     if (w < warp) before += x;

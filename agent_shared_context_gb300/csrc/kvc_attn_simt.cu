@@ -273,6 +273,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   s.group = s.tile = make_fastdiv(kTile);
   s.group_tiles = 1;
   s.even = 1;
+  s.overhead = 1;
   const int per_sm = smem * 2 + 4096 <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
   const int grid = di.sm_count * per_sm < kMaxCtas ? di.sm_count * per_sm : kMaxCtas;
   fn<<<grid, kThreads, smem, stream>>>(a, s);

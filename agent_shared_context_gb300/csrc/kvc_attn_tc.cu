@@ -64,8 +64,6 @@ using namespace ptx;
 using namespace attn;
 
 constexpr int kThreads = 384;              // 12 warps (roles above)
-constexpr int kRegsSoftmax = 208;          // 256 threads x 208 + 128 x 88 = 384 x 168, the launch's
-constexpr int kRegsOther = 88;
 constexpr int kRowsM = 128;                // rows of a stream (MMA M)
 constexpr int kTile = 128;                 // keys of a tile
 constexpr int kHalf = kTile / 2;           // keys of a step of a stream
@@ -74,6 +72,7 @@ constexpr int kSlotRows = 256;             // rows of a partial result
 constexpr int kMaxCtas = 160;
 constexpr int kItems = 4;                  // depth of the item ring
 constexpr int kNoPage = INT32_MIN;         // no key there: read as zeros
+constexpr int kItemCost = 6;               // tiles that an item's beginning and end cost
 constexpr float kLag = 8.0f;               // log2 by which m may lag behind
 constexpr float kHeavyPair = 0.125f;       // share of a row's sum that makes a key heavy
 constexpr float kHeavySingle = 0.0625f;
@@ -137,14 +136,16 @@ struct Bars {
   Shared sched;
 };
 
+// The waits.  What the first poll does not end goes on in a call, so that the
+// roles' loops stay small: an instruction cache holds them all.
+//
 // Counts the polls of a wait: every 4,096 of them it looks at the timer, which
 // costs hundreds of cycles, and at the abort flag, which it raises at the limit.
 struct Patience {
   uint64_t t0 = 0;
   uint32_t polls = 0;
-  __device__ __forceinline__ bool out(int32_t* abort_flag) {
+  __device__ __forceinline__ bool out(volatile int32_t* flag) {
     if ((++polls & 4095u) != 0u) return false;
-    volatile int32_t* flag = abort_flag;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
     if (t - t0 > kWaitLimitNs) *flag = 1;
@@ -152,34 +153,28 @@ struct Patience {
   }
 };
 
-// A whole warp waits for a phase: all lanes give up together.
-template <int NS>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b) {
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
   Patience p;
   bool ok = true;
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (p.out(&b->abort_flag)) {
-      ok = false;
-      break;
-    }
-  }
+  while (ok && !mbar_try_wait(bar, parity)) ok = !p.out(abort);
   return __all_sync(0xffffffffu, ok);
 }
 
-// A whole warp waits until *count, which another warp raises, has reached `want`.
+// A whole warp waits for a phase: all lanes give up together.
 template <int NS>
-__device__ __forceinline__ bool warp_wait_count(const volatile int32_t* count, int32_t want,
-                                                Bars<NS>* b) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<NS>* b) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, &b->abort_flag);
+}
+
+// A whole warp waits until *count, which another warp raises, has reached `want`.
+__device__ __noinline__ bool warp_wait_count(const volatile int32_t* count, int32_t want,
+                                             volatile int32_t* abort) {
   Patience p;
   bool ok = true;
 #pragma unroll 1
-  while (*count - want < 0) {
-    if (p.out(&b->abort_flag)) {
-      ok = false;
-      break;
-    }
-  }
+  while (ok && *count - want < 0) ok = !p.out(abort);
   __threadfence_block();
   return __all_sync(0xffffffffu, ok);
 }
@@ -195,6 +190,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
   return u;
 }
+
+// A value that all lanes hold, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
 
 // ------------------------------------------------------------ tile geometry
 // Ring positions, relative to the item's first: the order in which the MMAs
@@ -333,8 +331,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
 
-  if (warp >= 8) {
-  regs_lower<kRegsOther>();                       // one instruction for the whole warpgroup
   if (warp == 8) {
     // ------------------------------------------------------------ producer
     int ring = 0, n_items = 0;
@@ -453,15 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9 || warp == 11) {
     // ------------------------------------------------- MMAs of one stream
-    // Values that every MMA needs come from lane 0, so that they are uniform to
-    // the compiler too and stay in uniform registers.
-    const int st = __shfl_sync(0xffffffffu, warp == 9 ? 0 : 1, 0);
-    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    // Values that every MMA needs come out of a warp reduction: the compiler then
+    // knows that they are uniform and keeps the descriptors in uniform registers.
+    const int st = uniform(warp == 9 ? 0 : 1);
+    const uint32_t base = uniform(tmem);
     const uint32_t dS = base + st * 128, dO = base + 256 + st * D;
     // low words of the shared-memory descriptors
-    const uint64_t desc_q = desc_kmajor_sw128(smem_u32(q_smem));
-    const uint64_t desc_k = desc_kmajor_sw128(smem_u32(kv_smem));
-    const uint64_t desc_v = desc_mnmajor_sw128(smem_u32(kv_smem), kSubBytes);
+    const uint64_t desc_q = desc_kmajor_sw128(uniform(smem_u32(q_smem)));
+    const uint64_t desc_k = desc_kmajor_sw128(uniform(smem_u32(kv_smem)));
+    const uint64_t desc_v = desc_mnmajor_sw128(uniform(smem_u32(kv_smem)), kSubBytes);
     uint32_t ph_p = 0, ph_o = 0;
     bool ended = false;                            // an item's O may not be seen yet
     bool ok = true;
@@ -469,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = n_items % kItems;
       ok = warp_wait(&b->item_full[slot], (n_items / kItems) & 1, b);
       if (!ok) break;
-      const int n = __shfl_sync(0xffffffffu, b->items[slot].it.ntiles, 0);
+      const int n = uniform(b->items[slot].it.ntiles);
       if (n == 0) break;
-      const bool pair = __shfl_sync(0xffffffffu, b->items[slot].it.nt, 0) > p.tok_tile;
-      const int ring0 = __shfl_sync(0xffffffffu, b->items[slot].ring0, 0);
+      const bool pair = uniform(b->items[slot].it.nt) > p.tok_tile;
+      const int ring0 = uniform(b->items[slot].ring0);
       if (lane == 0) mbar_arrive(&b->item_empty[slot]);
       __syncwarp();
       const int first = pair ? 0 : st, step = pair ? 1 : 2;
@@ -538,12 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const volatile Told* told = &b->told[st][h];
-            const uint32_t heavy = told->heavy;
-            const bool acc = i > first + step || h > 0 || told->o_init != 0;
+            const uint32_t heavy = uniform(told->heavy);
+            const uint32_t acc = i > first + step || h > 0 ? 1u : uniform(told->o_init);
             const uint64_t dvh = dv + h * (kHalf * 128 >> 4);
-#pragma unroll
-            for (int k = 0; k < kHalf / 16; ++k)
-              mma_bf16_ts_warp(dO, tS_h + k * 8, dvh + k * (2048 >> 4), kIdescO, acc || k > 0);
+            static_assert(kHalf == 64, "four steps of 16 keys");
+            mma_bf16_ts_x4(dO, tS_h, dvh, kIdescO, acc);
             if (heavy != 0) {
               // the remainders of P, for the warps that have one in the step
 #pragma unroll 1
@@ -552,41 +547,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (who == 0) continue;
                 const uint32_t off[4] = {(who & 1u) - 1u, ((who >> 8) & 1u) - 1u,
                                          ((who >> 16) & 1u) - 1u, ((who >> 24) & 1u) - 1u};
-                mma_bf16_ts_warp_lanes(dO, tS_h + kHalf / 2 + k * 8, dvh + k * (2048 >> 4), kIdescO,
+                mma_bf16_ts_lanes(dO, tS_h + kHalf / 2 + k * 8, dvh + k * (2048 >> 4), kIdescO,
                                        off);
               }
             }
           }
           if (more) {
             const uint64_t dkh = dk + h * (kHalf * 128 >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int off = (k / 4) * (kSubBytes >> 4) + (k % 4) * 2;
-              mma_bf16_ss_warp(tS_h, dq + off, dkh + off, kIdescS, k > 0);
-            }
+            // 64 columns of d in each 128-byte row
+            mma_bf16_ss_x4(tS_h, dq, dkh, kIdescS, 0);
+            if (D == 128)
+              mma_bf16_ss_x4(tS_h, dq + (kSubBytes >> 4), dkh + (kSubBytes >> 4), kIdescS, 1);
           }
-          mma_commit_warp(&b->s_full[st][h]);
+          mma_commit_elect(&b->s_full[st][h]);
         }
         if (!ok) break;
         if (pv) {
           ph_p ^= 1;
-          mma_commit_warp(&b->kv_empty[v_at % NS]);
+          mma_commit_elect(&b->kv_empty[v_at % NS]);
         }
         if (!more) break;
-        mma_commit_warp(&b->kv_empty[k_at % NS]);
-        if (i + step >= n) mma_commit_warp(&b->q_empty);
+        mma_commit_elect(&b->kv_empty[k_at % NS]);
+        if (i + step >= n) mma_commit_elect(&b->q_empty);
       }
       if (ok && !pair) ok = pass_to(ring0 + 2 * n);
     }
     if (!ok) {
-      mma_commit_warp(&b->drain[st]);
+      mma_commit_elect(&b->drain[st]);
       mbar_wait_bounded(&b->drain[st], 0, kWaitLimitNs);
       __syncwarp();
     }
-  }
-  } else {
+  } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    regs_raise<kRegsSoftmax>();
     const int st = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;    // lane 32 w in bits 31-16
@@ -638,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t* bad = nullptr;                      // value rows that are added from memory
         if (edge) {
           const int slot_v = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
-          ok = warp_wait_count(&b->landed[st], n_tiles + k + 1, b);
+          ok = warp_wait_count(&b->landed[st], n_tiles + k + 1, &b->abort_flag);
           if (!ok) break;
           const TileSpan t = tile_span(p, it.tile0 + i);
           const Sight see = sight(a, it.kv, it.pos0, it.nt);
@@ -655,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto odd = [](uint32_t u) {                       // an exponent of all ones
             return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
           };
-#pragma unroll
+#pragma unroll 2
           for (int j = 0; j < D / 16; ++j) {
             int n;
             uint4* q = at(j, &n);
@@ -1023,6 +1015,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   s.group_tiles = a.B < kTile ? 1 : (a.B + kTile - 1) / kTile;
   s.tile = make_fastdiv(a.B < kTile ? group : kTile);
   s.even = s.group_tiles == 1 || a.B % kTile == 0;
+  s.overhead = kItemCost;
   p.out32 = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) && (a.o_tok * 2) % 32 == 0 &&
             (a.o_head * 2) % 32 == 0;
   p.ragged = p.has_holes || (a.B > kTile && a.B % kTile != 0);

@@ -189,36 +189,61 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // MMAs and the commit for a converged warp: every lane executes them with the
-// same operands and one elected lane issues.  An MMA issued under
-// `if (lane == 0)` costs some 170 cycles, because its descriptors cannot stay
-// in uniform registers; these cost about a quarter of that.
-__device__ __forceinline__ void mma_bf16_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
+// same operands, which the compiler should know to be uniform, and one elected
+// lane issues.  Four steps of K = 16 at a time: one election for them all.
+//
+// D[tmem] (+)= A[smem] * B[smem]^T over 64 columns of K, K-major operands.
+__device__ __forceinline__ void mma_bf16_ss_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t"
+      ".reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 2;\n\t"
+      "add.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\t"
+      "add.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\t"
+      "add.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-// A in TMEM: its rows in the lanes, two bf16 of K per 32-bit column.
-__device__ __forceinline__ void mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] over 64 rows of B (MN-major): A has its rows in
+// the lanes and two bf16 of K in each of 32 columns.
+__device__ __forceinline__ void mma_bf16_ts_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t"
+      ".reg .b32 a;\n\t"
+      ".reg .b64 b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\t"
+      "add.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\t"
+      "add.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\t"
+      "add.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-// The same, adding to the rows of the lanes whose bit in off[lane / 32] is 0.
-__device__ __forceinline__ void mma_bf16_ts_warp_lanes(uint32_t d_tmem, uint32_t a_tmem,
-                                                       uint64_t b_desc, uint32_t idesc,
-                                                       const uint32_t (&off)[4]) {
+// One step of it, adding to the rows of the lanes whose bit in off[lane / 32] is 0.
+__device__ __forceinline__ void mma_bf16_ts_lanes(uint32_t d_tmem, uint32_t a_tmem,
+                                                  uint64_t b_desc, uint32_t idesc,
+                                                  const uint32_t (&off)[4]) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -229,7 +254,7 @@ __device__ __forceinline__ void mma_bf16_ts_warp_lanes(uint32_t d_tmem, uint32_t
       : "memory");
 }
 
-__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -281,18 +306,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
-}
-
-// Moves registers between a block's warpgroups; every warp of a warpgroup
-// executes one of them.  The sum over the block must not exceed what the block
-// was launched with.
-template <int N>
-__device__ __forceinline__ void regs_raise() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_lower() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Thread i of the warp writes lane (taddr.lane + i), 32 consecutive columns.
