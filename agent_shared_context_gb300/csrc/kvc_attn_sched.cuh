@@ -246,7 +246,7 @@ struct Walker {
 };
 
 template <int THREADS>
-__device__ __forceinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_t* total) {
+__device__ __noinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -267,9 +267,77 @@ __device__ __forceinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_
   return v + before;
 }
 
-// Called by every thread of the CTA; the same walker in all of them.
+__device__ __forceinline__ Walker walker_empty(const SchedArgs& a, int64_t U) {
+  Walker w;
+  w.sh.U = U;
+  w.sh.n = static_cast<int>(U < gridDim.x ? U : gridDim.x);   // no empty shares between others:
+  w.sh.q = w.sh.n > 0 ? div64(U, w.sh.n) : 0;                 // an item's parts are consecutive
+  w.sh.rem = static_cast<int>(U - w.sh.q * w.sh.n);
+  w.sh.n_over_U = U > 0 ? __fdividef(static_cast<float>(w.sh.n), static_cast<float>(U)) : 0.f;
+  w.u = w.u1 = w.item_u0 = U;
+  w.r = a.R;
+  w.h = w.i = w.n = 0;
+  w.q = Request{0, 0, 0, 0};
+  return w;
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+  return __shfl_sync(0xffffffffu, v, lane);
+}
+
+// Up to 32 requests: a lane has one, and every warp finds the share by itself.
+static __device__ __noinline__ Walker walker_lanes(const SchedArgs& a, int32_t* dev_status) {
+  const int lane = threadIdx.x & 31;
+  Request q{0, 0, 0, 0};
+  int n = 0;
+  int64_t units = 0;
+  bool bad = false;
+  if (lane < a.R) {
+    q = load_request(a, lane, &bad);
+    n = n_items(a, q);
+    units = n == 1 ? item_units(a, q, 0) : first_units(a, q, n);
+  }
+  if (bad && blockIdx.x == 0) atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
+  const int64_t mine = units * a.H;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  Walker w = walker_empty(a, shfl64(incl, 31));
+  if (static_cast<int>(blockIdx.x) >= w.sh.n) return w;
+  w.u = w.sh.start(blockIdx.x);
+  w.u1 = w.sh.start(blockIdx.x + 1);
+  w.r = __ffs(__ballot_sync(0xffffffffu, incl > w.u)) - 1;
+  int64_t off = w.u - shfl64(incl - mine, w.r);
+  const int64_t hu = shfl64(units, w.r);
+  w.h = static_cast<int>(div64(off, hu));
+  off -= w.h * hu;
+  w.q.q0 = __shfl_sync(0xffffffffu, q.q0, w.r);
+  w.q.nq = __shfl_sync(0xffffffffu, q.nq, w.r);
+  w.q.kv = __shfl_sync(0xffffffffu, q.kv, w.r);
+  w.q.pos0 = __shfl_sync(0xffffffffu, q.pos0, w.r);
+  w.n = __shfl_sync(0xffffffffu, n, w.r);
+  w.item_u0 = w.u - off;
+  if (w.n > 1) {
+    // the last item that begins at or before `off`
+#pragma unroll 1
+    for (int base = 0; base < w.n; base += 32) {
+      const int64_t p = first_units(a, w.q, min(base + lane, w.n - 1));
+      const uint32_t before = __ballot_sync(0xffffffffu, base + lane < w.n && p <= off);
+      if (before == 0) break;
+      const int last = 31 - __clz(before);
+      w.i = base + last;
+      w.item_u0 = w.u - off + shfl64(p, last);
+    }
+  }
+  return w;
+}
+
+// More requests: a thread has one at a time.
 template <int THREADS>
-__device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_status) {
+__device__ __noinline__ Walker walker_block(const SchedArgs& a, Shared* sh, int32_t* dev_status) {
   const int tid = threadIdx.x;
   int64_t U = 0, mine = 0, incl = 0;
   bool bad = false;
@@ -285,19 +353,8 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
     U += total;
   }
   if (bad && blockIdx.x == 0) atomicCAS(dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
-  // no empty shares between others: an item's parts are consecutive CTAs
-  const int n = static_cast<int>(U < gridDim.x ? U : gridDim.x);
-  Walker w;
-  w.sh.U = U;
-  w.sh.n = n;
-  w.sh.q = n > 0 ? div64(U, n) : 0;
-  w.sh.rem = static_cast<int>(U - w.sh.q * n);
-  w.sh.n_over_U = U > 0 ? static_cast<float>(n) / static_cast<float>(U) : 0.f;
-  w.u = w.u1 = w.item_u0 = U;
-  w.r = a.R;
-  w.h = w.i = w.n = 0;
-  w.q = Request{0, 0, 0, 0};
-  if (static_cast<int>(blockIdx.x) >= n) return w;
+  Walker w = walker_empty(a, U);
+  if (static_cast<int>(blockIdx.x) >= w.sh.n) return w;
   w.u = w.sh.start(blockIdx.x);
   w.u1 = w.sh.start(blockIdx.x + 1);
   // the request of unit u ...
@@ -346,6 +403,14 @@ __device__ Walker walker_begin(const SchedArgs& a, Shared* sh, int32_t* dev_stat
     w.item_u0 = w.u - sh->item_off;
   }
   return w;
+}
+
+// Called by every thread of the CTA; the same walker in all of them.
+template <int THREADS>
+__device__ __forceinline__ Walker walker_begin(const SchedArgs& a, Shared* sh,
+                                               int32_t* dev_status) {
+  if (a.R <= 32) return walker_lanes(a, dev_status);
+  return walker_block<THREADS>(a, sh, dev_status);
 }
 
 // ------------------------------------------------------------ joining parts
