@@ -354,8 +354,9 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
   a.scale_log2 = at->scale * 1.4426950408889634f;
   a.workspace = workspace;
   a.dev_status = dev_status;
-  const cudaError_t e =
-      pg->dtype == KVC_BF16 ? launch_attn_tc(a, stream) : launch_attn_simt(a, stream);
+  const cudaError_t e = pg->dtype == KVC_F32    ? launch_attn_simt(a, stream)
+                        : attn_decode_fits(a) ? launch_attn_decode(a, stream)
+                                              : launch_attn_tc(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvc_paged_attention launch");
   return KVC_OK;
 }

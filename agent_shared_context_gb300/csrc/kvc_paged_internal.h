@@ -59,5 +59,8 @@ size_t attn_simt_workspace_bytes(int d);   // f32
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t stream);
 size_t attn_tc_workspace_bytes(int d);     // bf16, d = 64 or 128
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream);
+// bf16, decoding; its workspace is part of the one above.
+bool attn_decode_fits(const AttnArgs& a);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace kvc

@@ -198,6 +198,53 @@ def test_attention_divided_work(dtype, d, lens):
     assert torch.equal(first[0], b.out) and torch.equal(first[1], b.lse)
 
 
+# at most one new token per request on average: the decoding kernel
+DECODE = [(1, 1), (0, 70), (1, 33), (3, 130), (0, 0), (1, 259), (0, 5), (1, 128), (2, 700), (0, 1),
+          (0, 0), (1, 1025)]
+
+
+@pytest.mark.parametrize("B", [1, 7, 16, 48, 64, 128, 130, 1000])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 100)])
+def test_decode_page_sizes_and_masks(d, B, causal, window):
+    b = Batch(DECODE, 8, 2, d, B, "bf16", seed=B + window)
+    b.run(causal, window)
+    b.check(causal, window)
+
+
+@pytest.mark.parametrize("G", [1, 3, 4, 7, 8, 16])
+def test_decode_head_groups(G):
+    b = Batch(DECODE, 3 * G, 3, 128, 32, "bf16", seed=G, L=2, layer=1, layout="fused")
+    b.run()
+    b.check()
+
+
+def test_decode_one_request_among_idle_ones():
+    """A chunk of 60 tokens and 70 requests without any: many row tiles of the same request."""
+    b = Batch([(60, 500)] + [(0, 9)] * 70, 8, 2, 64, 16, "bf16", seed=2)
+    b.run()
+    b.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_decode_values_out_of_sight(d, value):
+    """As test_attention_values_out_of_sight, for a request with four tokens."""
+    b = Batch([(4, 200), (0, 0), (0, 3), (1, 77)], 4, 2, d, 16, "bf16", seed=4)
+    page, off = b.table[0, 199 // b.B], 199 % b.B
+    b.V[page, 0, :, off] = value
+    b.run()
+    torch.cuda.synchronize()
+    assert not b.out[3].isfinite().any()          # the last token sees it
+    b.V.copy_(b.host[1])
+    got = b.out.clone()
+    b.run()
+    torch.cuda.synchronize()
+    got[3] = b.out[3]
+    b.out.copy_(got)
+    b.check()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_large_and_shifted_scores(dtype):
     """Scores of +-100 that grow along the keys: the running maximum moves in every tile."""
