@@ -4,11 +4,13 @@
 // Decoding reads every key and value once and computes little with them: it is
 // bound by HBM, and a small batch by latency.  A row tile of 128 rows and a
 // pipeline of roles would be idle for the most part, so here a row tile has the
-// 16 rows of one warp-level MMA (m16n8k16) and every warp is on its own: it
+// 8 rows (16 where the group needs them) that a warp-level MMA (m16n8k16) takes
+// as its N, keys and columns of d being its M, and every warp is on its own: it
 // copies its 32 keys of a 128-key tile into its own ring in shared memory
-// (cp.async, three stages, no barrier with the other warps), multiplies them
-// with Q, which stays in registers, and keeps the running maximum, sum and
-// output of its keys.  The four warps' results are joined at the end of an item.
+// (cp.async, three stages, no barrier with the other warps), forms S^T = K Q^T
+// with Q^T in registers and O^T += V^T P^T, and keeps the running maximum, sum
+// and output of its keys.  The four warps' results are joined at the end of an
+// item.
 //
 // The mathematics is that of kvc_attn_simt.cu, P enters the product with V as
 // bf16(P) and the remainder P - bf16(P): the tensor core has time for both.
@@ -35,7 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;                  // keys of a warp's step
 constexpr int kTile = kKeys * kWarps;
-constexpr int kRows = 16;
+constexpr int kSlotRows = 16;              // rows of a partial result
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 320;
 constexpr int kItemCost = 2;
@@ -46,8 +48,9 @@ struct DecodeArgs {
   FastDiv page;
 };
 
-template <int D>
+template <int D, int NQ = 1>
 struct Cfg {
+  static constexpr int kRows = 8 * NQ;                            // rows of a tile
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalfStage = kKeys * kRowBytes;            // K or V of a step
   static constexpr int kWarpBytes = kStages * 2 * kHalfStage;
@@ -84,6 +87,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transposed 8 x 8 matrix of 16-bit elements, two to a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t u;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
@@ -103,10 +113,12 @@ __device__ __forceinline__ uint32_t at(int n, int u) {
   return static_cast<uint32_t>(n * Cfg<D>::kRowBytes + ((u ^ (n & 7)) << 4));
 }
 
-template <int D>
+// NQ: groups of eight rows of an item.
+template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
     attn_decode_kernel(const __grid_constant__ DecodeArgs p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, NQ>;
+  constexpr int kRows = C::kRows;
   constexpr int kUnits = D / 8;                    // 16-byte units of a row
   constexpr int kRowsAtOnce = 32 / kUnits;         // rows of a warp's 32 units
   extern __shared__ __align__(128) uint8_t smem[];
@@ -116,12 +128,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kWarpBytes;
   float* join = reinterpret_cast<float*>(smem + kWarps * C::kWarpBytes);
-  const int gr = lane >> 2, qc = lane & 3;         // row and column pair of an MMA fragment
+  const int gr = lane >> 2, qc = lane & 3;         // row and pair of columns of a fragment
 
   Walker w = walker_begin<kThreads>(p.s, &sched, a.dev_status);
   int32_t* counters = static_cast<int32_t*>(a.workspace);
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
-  const size_t slot_n = slot_floats(kRows, D);
+  const size_t slot_n = slot_floats(kSlotRows, D);
   const __nv_bfloat16* pools[2];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
@@ -181,39 +193,41 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       pages = next;
     }
 
-    // Q as the A operand: rows gr and gr + 8, two columns of each 8
-    uint32_t q[D / 16][4];
-    {
-      const __nv_bfloat16* qr[2];
-      bool has[2];
+    // Q^T as the B operand: row gr of each eight, two columns of each 8
+    uint32_t q[NQ][D / 16][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = gr + 8 * i, tok = row / a.G, g = row - tok * a.G;
-        has[i] = row < rows;
-        qr[i] = static_cast<const __nv_bfloat16*>(a.q) +
-                (has[i] ? (it.q0 + tok) * a.q_tok + (it.h * a.G + g) * a.q_head : 0);
-      }
+    for (int g8 = 0; g8 < NQ; ++g8) {
+      const int row = g8 * 8 + gr, tok = row / a.G, g = row - tok * a.G;
+      const bool has = row < rows;
+      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) +
+                                (has ? (it.q0 + tok) * a.q_tok + (it.h * a.G + g) * a.q_head : 0);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = c & 1, col = k * 16 + (c >> 1) * 8 + qc * 2;
-          q[k][c] = has[i] ? *reinterpret_cast<const uint32_t*>(qr[i] + col) : 0u;
-        }
+        for (int c = 0; c < 2; ++c)
+          q[g8][k][c] =
+              has ? *reinterpret_cast<const uint32_t*>(qr + k * 16 + c * 8 + qc * 2) : 0u;
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int key_lo[2], key_hi[2];
+    // of the rows 8 g8 + 2 qc and the next, which the lane's results belong to
+    float m[NQ][2], l[NQ][2];
+    int key_lo[NQ][2], key_hi[NQ][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int pos = it.pos0 + min((gr + 8 * i) / a.G, it.nt - 1);
-      key_hi[i] = a.causal ? min(it.kv, pos + 1) : it.kv;
-      key_lo[i] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    }
-    float o[D / 8][4];
+    for (int g8 = 0; g8 < NQ; ++g8)
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+      for (int i = 0; i < 2; ++i) {
+        const int pos = it.pos0 + min((g8 * 8 + qc * 2 + i) / a.G, it.nt - 1);
+        key_hi[g8][i] = a.causal ? min(it.kv, pos + 1) : it.kv;
+        key_lo[g8][i] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        m[g8][i] = -INFINITY;
+        l[g8][i] = 0.f;
+      }
+    float o[NQ][D / 16][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[n][c] = 0.f;
+    for (int g8 = 0; g8 < NQ; ++g8)
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[g8][n][c] = 0.f;
 
 #pragma unroll 1
     for (int t = 0; t < it.ntiles; ++t) {
@@ -225,64 +239,72 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       const int k0 = (it.tile0 + t) * kTile + warp * kKeys;
       const uint32_t sK = ring + (t % kStages) * 2 * C::kHalfStage, sV = sK + C::kHalfStage;
       if (k0 < any_hi && k0 + kKeys > any_lo) {
-        // S = Q K^T: four groups of eight keys
-        float s[4][4];
+        // S^T = K Q^T: two groups of sixteen keys
+        float s[NQ][2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int g8 = 0; g8 < NQ; ++g8)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[g8][n][c] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t b[4];       // keys 0-7 and 8-15 of the half, columns 0-7 and 8-15 of the step
-            ldmatrix4(sK + at<D>(half * 16 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)),
-                      b);
-            mma16816(s[2 * half], q[k], b[0], b[1]);
-            mma16816(s[2 * half + 1], q[k], b[2], b[3]);
+          for (int n = 0; n < 2; ++n) {
+            uint32_t f[4];       // keys 0-7, 8-15 with columns 0-7, then with columns 8-15
+            ldmatrix4(sK + at<D>(n * 16 + (lane & 15), 2 * k + (lane >> 4)), f);
+#pragma unroll
+            for (int g8 = 0; g8 < NQ; ++g8) mma16816(s[g8][n], f, q[g8][k][0], q[g8][k][1]);
           }
         const bool whole = k0 >= all_lo && k0 + kKeys <= all_hi;
-        if (!whole) {
+        uint32_t ph[NQ][2][2], pl[NQ][2][2];       // P^T and its remainder as B operands
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+        for (int g8 = 0; g8 < NQ; ++g8) {
+          if (!whole) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int tok = k0 + n * 8 + qc * 2 + (c & 1), i = c >> 1;
-              if (tok < key_lo[i] || tok >= key_hi[i]) s[n][c] = -INFINITY;
-            }
-        }
-        uint32_t ph[2][4], pl[2][4];               // P and its remainder as A operands
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) top = fmaxf(top, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float m_new = fmaxf(m[i], top * a.scale_log2);
-          const float ref = m_new == -INFINITY ? 0.f : m_new;
-          const float f = exp2_fast(m[i] - ref);
-          m[i] = m_new;
-          float sum = 0.f;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float p0 = exp2_fast(fmaf(s[n][2 * i], a.scale_log2, -ref));
-            const float p1 = exp2_fast(fmaf(s[n][2 * i + 1], a.scale_log2, -ref));
-            sum += p0 + p1;
-            s[n][2 * i] = p0;
-            s[n][2 * i + 1] = p1;
-            const uint32_t u = pack_bf16(p0, p1);
-            ph[n >> 1][(n & 1) * 2 + i] = u;
-            pl[n >> 1][(n & 1) * 2 + i] =
-                pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u));
+              for (int c = 0; c < 4; ++c) {
+                const int tok = k0 + n * 16 + (c >> 1) * 8 + gr, i = c & 1;
+                if (tok < key_lo[g8][i] || tok >= key_hi[g8][i]) s[g8][n][c] = -INFINITY;
+              }
           }
-          l[i] = l[i] * f + sum;
-          if (f != 1.f) {
+          float f[2];
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[n][2 * i] *= f;
-              o[n][2 * i + 1] *= f;
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(fmaxf(s[g8][0][i], s[g8][0][i + 2]), fmaxf(s[g8][1][i], s[g8][1][i + 2]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float m_new = fmaxf(m[g8][i], top * a.scale_log2);
+            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            f[i] = exp2_fast(m[g8][i] - ref);
+            m[g8][i] = m_new;
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int c = i; c < 4; c += 2) {
+                s[g8][n][c] = exp2_fast(fmaf(s[g8][n][c], a.scale_log2, -ref));
+                sum += s[g8][n][c];
+              }
+            l[g8][i] = l[g8][i] * f[i] + sum;
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = s[g8][n][2 * h], p1 = s[g8][n][2 * h + 1];
+              const uint32_t u = pack_bf16(p0, p1);
+              ph[g8][n][h] = transpose8x8(u);
+              pl[g8][n][h] = transpose8x8(
+                  pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u)));
             }
+          if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[g8][n][c] *= f[c & 1];
           }
         }
         // value rows that some rows see and others do not
@@ -304,41 +326,48 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
           odd = __any_sync(0xffffffffu, odd);
         }
         if (!odd) {
+          // O^T += V^T P^T
 #pragma unroll
           for (int n = 0; n < D / 16; ++n)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t b[4];     // 16 keys of the half, columns 0-7 and 8-15 of the group
-              ldmatrix4_trans(sV + at<D>(half * 16 + (lane & 15), 2 * n + (lane >> 4)), b);
-              mma16816(o[2 * n], ph[half], b[0], b[1]);
-              mma16816(o[2 * n], pl[half], b[0], b[1]);
-              mma16816(o[2 * n + 1], ph[half], b[2], b[3]);
-              mma16816(o[2 * n + 1], pl[half], b[2], b[3]);
+              uint32_t f[4];     // columns 0-7, 8-15 with keys 0-7, then with keys 8-15
+              ldmatrix4_trans(
+                  sV + at<D>(half * 16 + (lane & 7) + (lane >> 4) * 8, 2 * n + ((lane >> 3) & 1)), f);
+#pragma unroll
+              for (int g8 = 0; g8 < NQ; ++g8) {
+                mma16816(o[g8][n], f, ph[g8][half][0], ph[g8][half][1]);
+                mma16816(o[g8][n], f, pl[g8][half][0], pl[g8][half][1]);
+              }
             }
         } else {
 #pragma unroll 1
           for (int key = 0; key < kKeys; ++key) {
-            const int from = gr * 4 + ((key >> 1) & 3);      // lane with the key's P of row gr
-            float pk[2] = {0.f, 0.f};
+            const int from = (key & 7) * 4 + qc, tok = k0 + key;   // the lane with the key's P
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int g8 = 0; g8 < NQ; ++g8) {
+              float pk[2] = {0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float x = __shfl_sync(0xffffffffu, s[n][c], from);
-                if (n == (key >> 3) && (c & 1) == (key & 1)) pk[c >> 1] = x;
-              }
+              for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              uint32_t v;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(sV + at<D>(key, n) + qc * 4));
-              const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
+                for (int c = 0; c < 4; ++c) {
+                  const float x = __shfl_sync(0xffffffffu, s[g8][n][c], from);
+                  if (n * 2 + (c >> 1) == (key >> 3)) pk[c & 1] = x;
+                }
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int tok = k0 + key;
-                if (tok < key_lo[i] || tok >= key_hi[i]) continue;
-                o[n][2 * i] = fmaf(pk[i], v0, o[n][2 * i]);
-                o[n][2 * i + 1] = fmaf(pk[i], v1, o[n][2 * i + 1]);
-              }
+              for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint16_t v;
+                  asm volatile("ld.shared.b16 %0, [%1];"
+                               : "=h"(v)
+                               : "r"(sV + at<D>(key, 2 * n + h) + gr * 2));
+                  const float x = __uint_as_float(static_cast<uint32_t>(v) << 16);
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (tok >= key_lo[g8][i] && tok < key_hi[g8][i])
+                      o[g8][n][2 * h + i] = fmaf(pk[i], x, o[g8][n][2 * h + i]);
+                }
             }
           }
         }
@@ -348,22 +377,26 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
 
     // the four warps' rows
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int row = gr + 8 * i;
-      if (row < rows) {
-        float* mine = join + warp * kRows * (D + 2);
+    for (int g8 = 0; g8 < NQ; ++g8)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<float2*>(mine + row * D + n * 8 + qc * 2) =
-              make_float2(o[n][2 * i], o[n][2 * i + 1]);
-        if (qc == 0) {
-          mine[kRows * D + row] = m[i];
-          mine[kRows * D + kRows + row] = l[i];
+      for (int i = 0; i < 2; ++i) {
+        float sum = l[g8][i];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = g8 * 8 + qc * 2 + i;
+        if (row < rows) {
+          float* mine = join + warp * kRows * (D + 2);
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mine[row * D + n * 16 + h * 8 + gr] = o[g8][n][2 * h + i];
+          if (gr == 0) {
+            mine[kRows * D + row] = m[g8][i];
+            mine[kRows * D + kRows + row] = sum;
+          }
         }
       }
-    }
     __syncthreads();
     const bool whole_item = it.nparts == 1;
     float* part = slots + (static_cast<size_t>(blockIdx.x) * 2 + slot_of(it.part)) * slot_n;
@@ -399,10 +432,10 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
           a.lse[orow * (a.H * a.G) + head] =
               L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       } else {
-        *reinterpret_cast<float4*>(part + (c4 * kRows + row) * 4) = acc;
+        *reinterpret_cast<float4*>(part + (c4 * kSlotRows + row) * 4) = acc;
         if (c4 == 0) {
-          part[kRows * D + row] = M;
-          part[kRows * D + kRows + row] = L;
+          part[kSlotRows * D + row] = M;
+          part[kSlotRows * D + kSlotRows + row] = L;
         }
       }
     }
@@ -415,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       if (last) {
         __threadfence();
         if (threadIdx.x == 0) counters[it.cta0] = 0;
-        join_parts(slots, slot_n, kRows, 0, D, it, rows, threadIdx.x, kThreads,
+        join_parts(slots, slot_n, kSlotRows, 0, D, it, rows, threadIdx.x, kThreads,
                    [&](int row, int col, float4 v, float lse) {
                      const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                      const int64_t orow = it.q0 + tok;
@@ -431,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
   if (bad_page) atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
 }
 
-template <int D>
+template <int D, int NQ>
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
@@ -448,17 +481,17 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
   s.kv_cap = a.width * a.B;
   s.causal = a.causal;
   s.window = a.window;
-  s.item = make_fastdiv(kRows / a.G);
+  s.item = make_fastdiv(Cfg<D, NQ>::kRows / a.G);
   s.group = s.tile = make_fastdiv(kTile);
   s.group_tiles = 1;
   s.overhead = kItemCost;
   s.even = 1;
-  e = cudaFuncSetAttribute(attn_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<D>::kSmem);
+  e = cudaFuncSetAttribute(attn_decode_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<D, NQ>::kSmem);
   if (e != cudaSuccess) return e;
   const int most = di.sm_count * (D == 128 ? 1 : 2);
-  attn_decode_kernel<D>
-      <<<most < kMaxCtas ? most : kMaxCtas, kThreads, Cfg<D>::kSmem, stream>>>(p);
+  attn_decode_kernel<D, NQ>
+      <<<most < kMaxCtas ? most : kMaxCtas, kThreads, Cfg<D, NQ>::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -466,10 +499,12 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
 
 // At most one new token per request on average, all query heads of a KV head in
 // one row tile.
-bool attn_decode_fits(const AttnArgs& a) { return a.N <= a.R && a.G <= kRows; }
+bool attn_decode_fits(const AttnArgs& a) { return a.N <= a.R && a.G <= 16; }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
-  return a.d == 128 ? launch_decode<128>(a, stream) : launch_decode<64>(a, stream);
+  if (a.d == 128)
+    return a.G <= 8 ? launch_decode<128, 1>(a, stream) : launch_decode<128, 2>(a, stream);
+  return a.G <= 8 ? launch_decode<64, 1>(a, stream) : launch_decode<64, 2>(a, stream);
 }
 
 }  // namespace kvc
