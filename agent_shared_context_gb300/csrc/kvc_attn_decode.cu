@@ -36,6 +36,7 @@ using namespace attn;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;                  // keys of a warp's step
+constexpr int kG = kKeys / 16;             // groups of 16, the MMA's M
 constexpr int kTile = kKeys * kWarps;
 constexpr int kSlotRows = 16;              // rows of a partial result
 constexpr int kStages = 3;
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
   constexpr int kRows = C::kRows;
   constexpr int kUnits = D / 8;                    // 16-byte units of a row
   constexpr int kRowsAtOnce = 32 / kUnits;         // rows of a warp's 32 units
+  static_assert(kKeys <= 32 && kKeys % 16 == 0, "a lane looks up a key's page");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sched;
   __shared__ int32_t last;
@@ -154,13 +156,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
     // page of the lane's key of step t (-1: not to be read)
     auto page_of = [&](int t) -> int {
       const int tok = (it.tile0 + t) * kTile + warp * kKeys + lane;
-      return t < it.ntiles && tok >= any_lo && tok < any_hi ? __ldg(table + fast_div(tok, p.page))
+      return t < it.ntiles && lane < kKeys && tok >= any_lo && tok < any_hi ? __ldg(table + fast_div(tok, p.page))
                                                             : -1;
     };
     auto issue = [&](int t, int page) {
       if (t < it.ntiles) {
         const int tok = (it.tile0 + t) * kTile + warp * kKeys + lane;
-        const bool seen = tok >= any_lo && tok < any_hi;
+        const bool seen = lane < kKeys && tok >= any_lo && tok < any_hi;
         if (seen && (page < 0 || page >= a.P)) {
           bad_page = true;
           page = -1;
@@ -239,30 +241,30 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       const int k0 = (it.tile0 + t) * kTile + warp * kKeys;
       const uint32_t sK = ring + (t % kStages) * 2 * C::kHalfStage, sV = sK + C::kHalfStage;
       if (k0 < any_hi && k0 + kKeys > any_lo) {
-        // S^T = K Q^T: two groups of sixteen keys
-        float s[NQ][2][4];
+        // S^T = K Q^T
+        float s[NQ][kG][4];
 #pragma unroll
         for (int g8 = 0; g8 < NQ; ++g8)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kG; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[g8][n][c] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < kG; ++n) {
             uint32_t f[4];       // keys 0-7, 8-15 with columns 0-7, then with columns 8-15
             ldmatrix4(sK + at<D>(n * 16 + (lane & 15), 2 * k + (lane >> 4)), f);
 #pragma unroll
             for (int g8 = 0; g8 < NQ; ++g8) mma16816(s[g8][n], f, q[g8][k][0], q[g8][k][1]);
           }
         const bool whole = k0 >= all_lo && k0 + kKeys <= all_hi;
-        uint32_t ph[NQ][2][2], pl[NQ][2][2];       // P^T and its remainder as B operands
+        uint32_t ph[NQ][kG][2], pl[NQ][kG][2];       // P^T and its remainder as B operands
 #pragma unroll
         for (int g8 = 0; g8 < NQ; ++g8) {
           if (!whole) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kG; ++n)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int tok = k0 + n * 16 + (c >> 1) * 8 + gr, i = c & 1;
@@ -272,7 +274,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
           float f[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(fmaxf(s[g8][0][i], s[g8][0][i + 2]), fmaxf(s[g8][1][i], s[g8][1][i + 2]));
+            float top = fmaxf(s[g8][0][i], s[g8][0][i + 2]);
+#pragma unroll
+            for (int n = 1; n < kG; ++n) top = fmaxf(top, fmaxf(s[g8][n][i], s[g8][n][i + 2]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
             m[g8][i] = m_new;
             float sum = 0.f;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kG; ++n)
 #pragma unroll
               for (int c = i; c < 4; c += 2) {
                 s[g8][n][c] = exp2_fast(fmaf(s[g8][n][c], a.scale_log2, -ref));
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
             l[g8][i] = l[g8][i] * f[i] + sum;
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kG; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float p0 = s[g8][n][2 * h], p1 = s[g8][n][2 * h + 1];
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
 #pragma unroll
           for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kG; ++half) {
               uint32_t f[4];     // columns 0-7, 8-15 with keys 0-7, then with keys 8-15
               ldmatrix4_trans(
                   sV + at<D>(half * 16 + (lane & 7) + (lane >> 4) * 8, 2 * n + ((lane >> 3) & 1)), f);
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
             for (int g8 = 0; g8 < NQ; ++g8) {
               float pk[2] = {0.f, 0.f};
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+              for (int n = 0; n < kG; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                   const float x = __shfl_sync(0xffffffffu, s[g8][n][c], from);
