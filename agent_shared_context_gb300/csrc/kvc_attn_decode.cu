@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
           }
         }
       }
+    parts(w, &it);
     __syncthreads();
     const bool whole_item = it.nparts == 1;
     float* part = slots + (static_cast<size_t>(blockIdx.x) * 2 + slot_of(it.part)) * slot_n;

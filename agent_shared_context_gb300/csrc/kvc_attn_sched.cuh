@@ -171,21 +171,18 @@ static __device__ __noinline__ int64_t div64(int64_t x, int64_t y) {
 
 // U units cut into n shares [c U / n, (c + 1) U / n).
 struct Shares {
-  int64_t U, q;                // all units, U / n
-  int32_t n, rem;              // shares, U % n
-  float n_over_U;
+  int64_t U;
+  int32_t n;
 
   __device__ __forceinline__ int64_t start(int c) const {
-    return c * q + static_cast<uint32_t>(c * rem) / static_cast<uint32_t>(n);
+    const int64_t x = c * U;
+    if (x < (int64_t(1) << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(n);
+    return x / n;
   }
-  // The share of unit u: an estimate, then a step or two to the exact one.
   __device__ __forceinline__ int owner(int64_t u) const {
-    int c = min(n - 1, static_cast<int>(static_cast<float>(u) * n_over_U));
-#pragma unroll 1
-    while (c > 0 && start(c) > u) --c;
-#pragma unroll 1
-    while (c + 1 < n && start(c + 1) <= u) ++c;
-    return c;
+    const int64_t x = (u + 1) * n - 1;
+    if (x < (int64_t(1) << 32)) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(U));
+    return static_cast<int>(x / U);
   }
 };
 
@@ -197,6 +194,8 @@ struct Walker {
   int64_t item_u0;             // first unit of that item
   Request q;
   int32_t n;                   // items of request r
+  int64_t item_first, item_end;   // units of the last part's item, and whether it is all
+  bool begins, ends;              // here: what parts() goes by
 
   // Next part of the share; false at its end.
   __device__ __forceinline__ bool next(const SchedArgs& a, Item* out) {
@@ -220,11 +219,10 @@ struct Walker {
           out->pos0 = q.pos0 + t0;
           out->tile0 = lo + static_cast<int>(u - first);
           out->ntiles = static_cast<int>(stop - u);
-          const int me = blockIdx.x;
-          const int c0 = u == first ? me : sh.owner(first);
-          out->cta0 = c0;
-          out->part = me - c0;
-          out->nparts = (end <= u1 ? me : sh.owner(end - 1)) - c0 + 1;
+          begins = u == first;
+          ends = end <= u1;
+          item_first = first;
+          item_end = end;
           u = stop;
           return true;
         }
@@ -244,6 +242,14 @@ struct Walker {
     }
   }
 };
+
+// The part that next() gave among its item's.
+__device__ __forceinline__ void parts(const Walker& w, Item* it) {
+  const int me = blockIdx.x;
+  it->cta0 = w.begins ? me : w.sh.owner(w.item_first);
+  it->part = me - it->cta0;
+  it->nparts = (w.ends ? me : w.sh.owner(w.item_end - 1)) - it->cta0 + 1;
+}
 
 template <int THREADS>
 __device__ __noinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_t* total) {
@@ -270,14 +276,14 @@ __device__ __noinline__ int64_t block_inclusive(int64_t v, Shared* sh, int64_t* 
 __device__ __forceinline__ Walker walker_empty(const SchedArgs& a, int64_t U) {
   Walker w;
   w.sh.U = U;
-  w.sh.n = static_cast<int>(U < gridDim.x ? U : gridDim.x);   // no empty shares between others:
-  w.sh.q = w.sh.n > 0 ? div64(U, w.sh.n) : 0;                 // an item's parts are consecutive
-  w.sh.rem = static_cast<int>(U - w.sh.q * w.sh.n);
-  w.sh.n_over_U = U > 0 ? __fdividef(static_cast<float>(w.sh.n), static_cast<float>(U)) : 0.f;
+  // no empty shares between others: an item's parts are consecutive CTAs
+  w.sh.n = static_cast<int>(U < gridDim.x ? U : gridDim.x);
   w.u = w.u1 = w.item_u0 = U;
   w.r = a.R;
   w.h = w.i = w.n = 0;
   w.q = Request{0, 0, 0, 0};
+  w.item_first = w.item_end = 0;
+  w.begins = w.ends = true;
   return w;
 }
 

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
 
   Item it;
   while (w.next(sa, &it)) {
+    parts(w, &it);
     const int rows = it.nt * a.G;
     // the item's query rows; rows past the item are zero
     for (int i = tid; i < kRows * dv; i += kThreads) {

@@ -349,7 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = n_items % kItems;
       ok = warp_wait(&b->item_empty[slot], ((n_items / kItems) & 1) ^ 1, b);
       if (!ok) break;
-      if (!more) it.ntiles = 0;
+      if (more)
+        parts(w, &it);
+      else
+        it.ntiles = 0;
       int edge_lo = 0, edge_hi = 0;
       if (more) edges(p.s, sight(a, it.kv, it.pos0, it.nt), &edge_lo, &edge_hi);
       if (lane == 0) {
