@@ -448,6 +448,13 @@ def test_plan_edges():
     two = np.array([[3, 2, 1, 0], [-1, -1, -1, -1]])
     _check_plan(16, [-1, 60], [50, 0], two, f, 0, 60, 8)        # the returned pages serve the next
     _check_plan(1 << 20, [1000000], [5], z[:, :2], f, 1, 1000000, 8)
+    # lengths whose sum runs over 31 bits: only the requests that they belong to are refused
+    huge = 2 ** 31 - 1
+    four = np.full((4, 4), -1)
+    _check_plan(16, [5, huge, huge, 0], [0, 0, 0, 0], four, f, 8, 40, 8)
+    _check_plan(16, [5, 40, huge, 3], [0, 0, 0, 0], four, f, 8, 45, 8)
+    _check_plan(16, [huge] * 600 + [3], [0] * 601, np.full((601, 2), -1), f, 8, 45, 8)
+    _check_plan(16, [3] + [huge] * 600, [0] * 601, np.full((601, 2), -1), f, 8, 45, 8)
 
 
 def test_plan_without_requests():
