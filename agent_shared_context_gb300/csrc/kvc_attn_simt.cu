@@ -8,7 +8,11 @@
 // key keeps m = -inf, l = 0 and gives out = 0, lse = -inf.
 //
 // A tile is 64 keys.  The rows of an item are (token, query head of the KV
-// head's group), so that K and V are read once for the whole group.
+// head's group), so that K and V are read once for the whole group.  256 threads
+// have 4 rows x 4 keys of the scores and 4 rows x 4 columns (per 64 of d) of the
+// output each, which asks shared memory for one 16-byte word per 8 FMAs.  The
+// next tile is copied (cp.async) while one is worked on, where d leaves room for
+// two; the pages of its rows are looked up a tile ahead of that.
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
 
@@ -31,21 +35,31 @@ __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<f
 struct Smem {
   Shared sched;
   int32_t last;
+  int64_t off[2][2][kTile];        // [parity][K or V][key]: element offset in its pool, -1: none
 };
 
-// RPT: rows per thread; an item has 16 * RPT rows.  DC:
-// 64-column groups of d per thread.
-template <int RPT, int DC>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, const SchedArgs sa) {
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool real) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  const int bytes = real ? 16 : 0;         // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// RPT: rows per thread; an item has 16 * RPT rows.  DC: 64-column groups of d per
+// thread.  ST: tiles in shared memory.
+template <int RPT, int DC, int ST>
+__global__ void __launch_bounds__(kThreads)
+    attn_simt_kernel(const AttnArgs a, const SchedArgs sa, const FastDiv per_page,
+                     const FastDiv per_row) {
   extern __shared__ float4 smem4[];
   __shared__ Smem sh;
   constexpr int kRows = 16 * RPT;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int d = a.d, dp = d + 4, dv = d >> 2;
   float* Qs = reinterpret_cast<float*>(smem4);      // [kRows][dp]
-  float* Ks = Qs + kRows * dp;                      // [kTile][dp]
-  float* Vs = Ks + kTile * dp;                      // [kTile][d]
-  float* Ps = Vs + kTile * d;                       // [kRows][kTile + 4]
+  float* Kt = Qs + kRows * dp;                      // [ST][kTile][dp]
+  float* Vt = Kt + ST * kTile * dp;                 // [ST][kTile][d]
+  float* Ps = Vt + ST * kTile * d;                  // [kRows][kTile + 4]
   constexpr int kPp = kTile + 4;
 
   Walker w = walker_begin<kThreads>(sa, &sh.sched, a.dev_status);
@@ -61,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
     const int rows = it.nt * a.G;
     // the item's query rows; rows past the item are zero
     for (int i = tid; i < kRows * dv; i += kThreads) {
-      const int row = i / dv, c = (i - row * dv) * 4;
+      const int row = fast_div(i, per_row), c = (i - row * dv) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < rows) {
         const int tok = row / a.G, g = row - tok * a.G;
@@ -85,30 +99,52 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
       for (int c = 0; c < DC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
+    const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
+    // where the rows of tile t lie
+    auto locate = [&](int t) {
+      const int n = tid & (kTile - 1), kv = tid / kTile;      // the first 128 threads
+      if (kv > 1 || t >= it.ntiles) return;
+      const int tok = (it.tile0 + t) * kTile + n;
+      int64_t off = -1;
+      if (tok < it.kv) {
+        const int blk = fast_div(tok, per_page);
+        const int page = __ldg(table + blk);
+        if (page >= 0 && page < a.P)
+          off = page * a.pool[kv].s_req + it.h * a.pool[kv].s_head +
+                static_cast<int64_t>(tok - blk * a.B) * a.pool[kv].s_tok;
+        else
+          atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
+      }
+      sh.off[t & 1][kv][n] = off;
+    };
+    auto copy = [&](int t) {
+      if (t < it.ntiles) {
+        float* Ks = Kt + (t % ST) * kTile * dp;
+        float* Vs = Vt + (t % ST) * kTile * d;
+        for (int i = tid; i < kTile * dv; i += kThreads) {
+          const int n = fast_div(i, per_row), c = (i - n * dv) * 4;
+          const int64_t ok = sh.off[t & 1][0][n], ov = sh.off[t & 1][1][n];
+          cp_async16(Ks + n * dp + c, poolK + (ok < 0 ? 0 : ok + c), ok >= 0);
+          cp_async16(Vs + n * d + c, poolV + (ov < 0 ? 0 : ov + c), ov >= 0);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    locate(0);
+    if (ST > 1) {
+      locate(1);
+      __syncthreads();
+      copy(0);
+    }
     for (int t = 0; t < it.ntiles; ++t) {
       const int k0 = (it.tile0 + t) * kTile;
+      const float* Ks = Kt + (t % ST) * kTile * dp;
+      const float* Vs = Vt + (t % ST) * kTile * d;
       __syncthreads();                          // the previous tile has been read
-      for (int i = tid; i < kTile * dv; i += kThreads) {
-        const int n = i / dv, c = (i - n * dv) * 4;
-        const int tok = k0 + n;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (tok < it.kv) {
-          const int blk = tok / a.B;
-          const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
-          if (page >= 0 && page < a.P) {
-            const int64_t off = tok - blk * a.B;
-            k = load4(poolK + page * a.pool[0].s_req + it.h * a.pool[0].s_head +
-                      off * a.pool[0].s_tok + c);
-            v = load4(poolV + page * a.pool[1].s_req + it.h * a.pool[1].s_head +
-                      off * a.pool[1].s_tok + c);
-          } else {
-            atomicCAS(a.dev_status, 0, static_cast<int32_t>(KVC_ERR_SHAPE));
-          }
-        }
-        *reinterpret_cast<float4*>(Ks + n * dp + c) = k;
-        *reinterpret_cast<float4*>(Vs + n * d + c) = v;
-      }
+      copy(ST > 1 ? t + 1 : t);
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
       __syncthreads();
+      locate(t + ST);
 
       float s[RPT][4];
 #pragma unroll
@@ -169,23 +205,47 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
         }
       }
       __syncwarp();                             // a warp reads the P rows it wrote
-      for (int n = 0; n < kTile; ++n) {
-        float p[RPT];
+      if (whole) {
+        for (int n = 0; n < kTile; n += 4) {
+          float4 p[RPT];
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) p[i] = Ps[(ty * RPT + i) * kPp + n];
+          for (int i = 0; i < RPT; ++i)
+            p[i] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + i) * kPp + n);
 #pragma unroll
-        for (int c = 0; c < DC; ++c) {
-          const int col = tx * 4 + c * 64;
-          if (col < d) {
-            const float4 v = *reinterpret_cast<const float4*>(Vs + n * d + col);
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-              // a key out of a row's sight adds nothing, whatever its value row holds
-              if (!whole && !(k0 + n >= key_lo[i] && k0 + n < key_hi[i])) continue;
-              o[i][c].x = fmaf(p[i], v.x, o[i][c].x);
-              o[i][c].y = fmaf(p[i], v.y, o[i][c].y);
-              o[i][c].z = fmaf(p[i], v.z, o[i][c].z);
-              o[i][c].w = fmaf(p[i], v.w, o[i][c].w);
+            for (int c = 0; c < DC; ++c) {
+              const int col = tx * 4 + c * 64;
+              if (col < d) {
+                const float4 v = *reinterpret_cast<const float4*>(Vs + (n + j) * d + col);
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                  const float q = j == 0 ? p[i].x : j == 1 ? p[i].y : j == 2 ? p[i].z : p[i].w;
+                  o[i][c].x = fmaf(q, v.x, o[i][c].x);
+                  o[i][c].y = fmaf(q, v.y, o[i][c].y);
+                  o[i][c].z = fmaf(q, v.z, o[i][c].z);
+                  o[i][c].w = fmaf(q, v.w, o[i][c].w);
+                }
+              }
+            }
+        }
+      } else {
+        for (int n = 0; n < kTile; ++n) {
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) {
+            // a key out of a row's sight adds nothing, whatever its value row holds
+            if (!(k0 + n >= key_lo[i] && k0 + n < key_hi[i])) continue;
+            const float q = Ps[(ty * RPT + i) * kPp + n];
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+              const int col = tx * 4 + c * 64;
+              if (col < d) {
+                const float4 v = *reinterpret_cast<const float4*>(Vs + n * d + col);
+                o[i][c].x = fmaf(q, v.x, o[i][c].x);
+                o[i][c].y = fmaf(q, v.y, o[i][c].y);
+                o[i][c].z = fmaf(q, v.z, o[i][c].z);
+                o[i][c].w = fmaf(q, v.w, o[i][c].w);
+              }
             }
           }
         }
@@ -249,17 +309,18 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a, c
   }
 }
 
-template <int RPT, int DC>
-cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
-  if (e != cudaSuccess) return e;
+size_t smem_bytes(int rows, int d, int tiles) {
+  return sizeof(float) * (static_cast<size_t>(rows) * (d + 4) +
+                          static_cast<size_t>(tiles) * kTile * (2 * d + 4) + rows * (kTile + 4));
+}
+
+template <int RPT, int DC, int ST>
+cudaError_t launch_one(const AttnArgs& a, const DeviceInfo& di, cudaStream_t stream) {
   const int rows = 16 * RPT;
-  const size_t smem = sizeof(float) * (static_cast<size_t>(rows) * (a.d + 4) + kTile * (a.d + 4) +
-                                       kTile * a.d + rows * (kTile + 4));
-  auto* fn = attn_simt_kernel<RPT, DC>;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem));
+  const size_t smem = smem_bytes(rows, a.d, ST);
+  auto* fn = attn_simt_kernel<RPT, DC, ST>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   SchedArgs s{};
   s.q_start = a.q_start;
@@ -275,19 +336,30 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
   s.group_tiles = 1;
   s.even = 1;
   s.overhead = 1;
-  const int per_sm = smem * 2 + 4096 <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
+  const int per_sm = 2 * (smem + sizeof(Smem) + 1024) <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
   const int grid = di.sm_count * per_sm < kMaxCtas ? di.sm_count * per_sm : kMaxCtas;
-  fn<<<grid, kThreads, smem, stream>>>(a, s);
+  fn<<<grid, kThreads, smem, stream>>>(a, s, make_fastdiv(a.B), make_fastdiv(a.d / 4));
   return cudaGetLastError();
+}
+
+// Two tiles where they fit in shared memory.
+template <int RPT, int DC>
+cudaError_t launch_st(const AttnArgs& a, cudaStream_t stream) {
+  DeviceInfo di;
+  const cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  if (smem_bytes(16 * RPT, a.d, 2) + sizeof(Smem) + 1024 <= static_cast<size_t>(di.max_smem_optin))
+    return launch_one<RPT, DC, 2>(a, di, stream);
+  return launch_one<RPT, DC, 1>(a, di, stream);
 }
 
 template <int RPT>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t stream) {
   switch ((a.d + 63) / 64) {
-    case 1: return launch_one<RPT, 1>(a, stream);
-    case 2: return launch_one<RPT, 2>(a, stream);
-    case 3: return launch_one<RPT, 3>(a, stream);
-    default: return launch_one<RPT, 4>(a, stream);
+    case 1: return launch_st<RPT, 1>(a, stream);
+    case 2: return launch_st<RPT, 2>(a, stream);
+    case 3: return launch_st<RPT, 3>(a, stream);
+    default: return launch_st<RPT, 4>(a, stream);
   }
 }
 

@@ -247,11 +247,16 @@ constexpr int kWriteThreads = 256;
 constexpr int kWriteVecs = 4;                    // vectors per thread, all in flight
 
 // One CTA copies a run of rows of one (layer, head) of K or V.  Bound by HBM:
-// each 16-byte vector is read once and written once.
-__global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const WriteArgs a) {
+// each 16-byte vector is read once and written once, past the caches.  BIG: row
+// or slot numbers beyond 31 bits (64-bit divisions made the copy wait for
+// arithmetic: two trajectories of 10,240 tokens took 1,051 us with them).
+template <bool BIG>
+__global__ void __launch_bounds__(kWriteThreads)
+    page_write_kernel(const WriteArgs a, const FastDiv per_src, const FastDiv per_page,
+                      const FastDiv per_row) {
   const int kv = blockIdx.z;
   const int l = blockIdx.y / a.H, h = blockIdx.y - l * a.H;
-  const int64_t rows_cta = kWriteThreads * kWriteVecs / a.vec_row;
+  const int rows_cta = kWriteThreads * kWriteVecs / a.vec_row;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
   const int64_t e = a.elem;
   const char* src = static_cast<const char*>(a.src[kv].base) +
@@ -259,27 +264,31 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const WriteAr
   char* pool = static_cast<char*>(a.pool[kv].base) +
                ((a.L0 + l) * a.pool[kv].s_layer + h * a.pool[kv].s_head) * e;
   uint4 v[kWriteVecs];
-  int64_t at[kWriteVecs];
+  int64_t slot[kWriteVecs];
+  int col[kWriteVecs];
 #pragma unroll
   for (int k = 0; k < kWriteVecs; ++k) {
     const int i = threadIdx.x + k * kWriteThreads;
-    const int row = i / a.vec_row, c = i - row * a.vec_row;
+    const int row = fast_div(i, per_row);
+    col[k] = (i - row * a.vec_row) * 16;
     const int64_t n = row0 + row;
-    at[k] = -1;
+    slot[k] = -1;
     if (row < rows_cta && n < a.rows) {
-      const int64_t slot = a.slots[n];
-      if (slot >= 0 && slot < a.n_slots) {
-        const int64_t r = n / a.T, t = n - r * a.T;
-        v[k] = *reinterpret_cast<const uint4*>(
-            src + (r * a.src[kv].s_req + t * a.src[kv].s_tok) * e + c * 16);
-        const int64_t page = slot / a.B;
-        at[k] = (page * a.pool[kv].s_req + (slot - page * a.B) * a.pool[kv].s_tok) * e + c * 16;
-      }
+      slot[k] = __ldg(a.slots + n);
+      const int64_t r = BIG ? n / a.T : fast_div(static_cast<int>(n), per_src);
+      v[k] = __ldcs(reinterpret_cast<const uint4*>(
+          src + (r * a.src[kv].s_req + (n - r * a.T) * a.src[kv].s_tok) * e + col[k]));
     }
   }
 #pragma unroll
-  for (int k = 0; k < kWriteVecs; ++k)
-    if (at[k] >= 0) *reinterpret_cast<uint4*>(pool + at[k]) = v[k];
+  for (int k = 0; k < kWriteVecs; ++k) {
+    if (slot[k] < 0 || slot[k] >= a.n_slots) continue;
+    const int64_t page = BIG ? slot[k] / a.B : fast_div(static_cast<int>(slot[k]), per_page);
+    __stcs(reinterpret_cast<uint4*>(
+               pool + (page * a.pool[kv].s_req + (slot[k] - page * a.B) * a.pool[kv].s_tok) * e +
+               col[k]),
+           v[k]);
+  }
 }
 
 }  // namespace
@@ -313,7 +322,10 @@ cudaError_t launch_page_write(const WriteArgs& a, cudaStream_t stream) {
   const int64_t rows_cta = kWriteThreads * kWriteVecs / a.vec_row;
   const dim3 grid(static_cast<unsigned>((a.rows + rows_cta - 1) / rows_cta),
                   static_cast<unsigned>(a.nl * a.H), 2);
-  page_write_kernel<<<grid, kWriteThreads, 0, stream>>>(a);
+  const int64_t most = int64_t(1) << 31;
+  auto* fn = a.rows >= most || a.n_slots >= most ? page_write_kernel<true> : page_write_kernel<false>;
+  fn<<<grid, kWriteThreads, 0, stream>>>(a, attn::make_fastdiv(a.T), attn::make_fastdiv(a.B),
+                                         attn::make_fastdiv(a.vec_row));
   return cudaGetLastError();
 }
 

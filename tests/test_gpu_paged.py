@@ -496,6 +496,20 @@ def test_write_rows(dtype, d, n, T, nl, H, B):
             assert np.array_equal(x.float().cpu().numpy(), want)
 
 
+def test_write_slots_beyond_31_bits():
+    """Rows of 16 bytes: over 2^31 slots in 34 GB a pool."""
+    kvc = _kvc()
+    P, B = (1 << 24) + 9, 128
+    pools = [torch.empty((P, 1, 1, B, 4), device="cuda") for _ in "KV"]
+    slots = torch.tensor([[0, P * B - 1, (1 << 31) + 77, P * B, -1, 1 << 31, (1 << 31) - 1]], device="cuda")
+    src = [torch.randn((1, 1, 1, 7, 4), device="cuda") for _ in "KV"]
+    kvc.kvc_page_write(kvc.paged(P, B, 1, 1, 4, "f32", 1, 1), src[0], src[1], slots, pools[0], pools[1])
+    for pool, s in zip(pools, src):
+        for i in (0, 1, 2, 5, 6):
+            at = int(slots[0, i])
+            assert torch.equal(pool[at // B, 0, 0, at % B], s[0, 0, 0, i])
+
+
 def test_write_into_token_major_pools():
     kvc = _kvc()
     both = torch.zeros((6, 2, 16, 2, 4, 64), dtype=torch.bfloat16, device="cuda")   # [P, K|V, B, L, H, d]
