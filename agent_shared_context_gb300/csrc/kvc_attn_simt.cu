@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kThreads)
       }
       *reinterpret_cast<float4*>(Qs + row * dp + c) = v;
     }
+    const int all_hi = a.causal ? min(it.kv, it.pos0 + 1) : it.kv;      // keys that all rows see
+    const int all_lo = a.window > 0 ? max(0, it.pos0 + it.nt - a.window) : 0;
     float m[RPT], l[RPT];
     int key_lo[RPT], key_hi[RPT];              // keys in sight of the thread's rows
     float4 o[RPT][DC];
@@ -168,7 +170,17 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
       }
-      bool whole = true;                        // every row of the thread sees the whole tile
+      // A tile that some rows do not see whole: an infinity or a NaN among its values must
+      // not meet the zeros of those rows.
+      bool odd = false;
+      if (k0 < all_lo || k0 + kTile > all_hi) {
+        for (int i = tid; i < kTile * dv; i += kThreads) {
+          const float4 v = *reinterpret_cast<const float4*>(Vs + i * 4);
+          // 0 times each is 0, or NaN
+          odd = odd || (v.x * 0.f + v.y * 0.f) + (v.z * 0.f + v.w * 0.f) != 0.f;
+        }
+        odd = __syncthreads_or(odd);
+      }
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
         float mx = -INFINITY;
@@ -179,7 +191,6 @@ __global__ void __launch_bounds__(kThreads)
           s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
           mx = fmaxf(mx, s[i][j]);
         }
-        whole = whole && (ty * RPT + i >= rows || (k0 >= key_lo[i] && k0 + kTile <= key_hi[i]));
 #pragma unroll
         for (int b = 8; b > 0; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
         const float m_new = fmaxf(m[i], mx);
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       __syncwarp();                             // a warp reads the P rows it wrote
-      if (whole) {
+      if (!odd) {
         for (int n = 0; n < kTile; n += 4) {
           float4 p[RPT];
 #pragma unroll
