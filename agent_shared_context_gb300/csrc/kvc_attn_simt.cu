@@ -15,6 +15,7 @@
 // two; the pages of its rows are looked up a tile ahead of that.
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
+#include "kvc_ptx.cuh"
 
 namespace kvc {
 namespace {
@@ -31,6 +32,17 @@ __device__ __forceinline__ float4 load4(const float* p) {
 }
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
+__device__ __forceinline__ uint64_t twice(float x) {
+  return ptx::pack_f32x2(__float_as_uint(x), __float_as_uint(x));
+}
+
+__device__ __forceinline__ float4 as_float4(uint64_t lo, uint64_t hi) {
+  float4 v;
+  ptx::unpack_f32x2(lo, v.x, v.y);
+  ptx::unpack_f32x2(hi, v.z, v.w);
+  return v;
+}
 
 struct Smem {
   Shared sched;
@@ -88,7 +100,7 @@ __global__ void __launch_bounds__(kThreads)
     const int all_lo = a.window > 0 ? max(0, it.pos0 + it.nt - a.window) : 0;
     float m[RPT], l[RPT];
     int key_lo[RPT], key_hi[RPT];              // keys in sight of the thread's rows
-    float4 o[RPT][DC];
+    uint64_t o[RPT][DC][2];                    // four columns in two pairs
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int row = ty * RPT + i;
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(kThreads)
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < DC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < DC; ++c) o[i][c][0] = o[i][c][1] = 0;
     }
 
     const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
@@ -148,28 +160,35 @@ __global__ void __launch_bounds__(kThreads)
       __syncthreads();
       locate(t + ST);
 
+      // two columns of d at a time (fma.f32x2): even and odd ones add up apart
+      uint64_t s2[RPT][4];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+#pragma unroll 2
+      for (int c = 0; c < d; c += 4) {
+        ulonglong2 kq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          kq[j] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * j) * dp + c);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(Qs + (ty * RPT + i) * dp + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s2[i][j] = ptx::fma_f32x2(q.y, kq[j].y, ptx::fma_f32x2(q.x, kq[j].x, s2[i][j]));
+        }
+      }
       float s[RPT][4];
 #pragma unroll
       for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-      for (int c = 0; c < d; c += 4) {
-        float4 kq[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          kq[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * dp + c);
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-          const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * RPT + i) * dp + c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(q.x, kq[j].x, s[i][j]);
-            s[i][j] = fmaf(q.y, kq[j].y, s[i][j]);
-            s[i][j] = fmaf(q.z, kq[j].z, s[i][j]);
-            s[i][j] = fmaf(q.w, kq[j].w, s[i][j]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          float even, uneven;
+          ptx::unpack_f32x2(s2[i][j], even, uneven);
+          s[i][j] = even + uneven;
         }
-      }
       // A tile that some rows do not see whole: an infinity or a NaN among its values must
       // not meet the zeros of those rows.
       bool odd = false;
@@ -209,10 +228,9 @@ __global__ void __launch_bounds__(kThreads)
         m[i] = m_new;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
-          o[i][c].x *= f;
-          o[i][c].y *= f;
-          o[i][c].z *= f;
-          o[i][c].w *= f;
+          const uint64_t f2 = twice(f);
+          o[i][c][0] = ptx::mul_f32x2(o[i][c][0], f2);
+          o[i][c][1] = ptx::mul_f32x2(o[i][c][1], f2);
         }
       }
       __syncwarp();                             // a warp reads the P rows it wrote
@@ -228,14 +246,13 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 0; c < DC; ++c) {
               const int col = tx * 4 + c * 64;
               if (col < d) {
-                const float4 v = *reinterpret_cast<const float4*>(Vs + (n + j) * d + col);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(Vs + (n + j) * d + col);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                  const float q = j == 0 ? p[i].x : j == 1 ? p[i].y : j == 2 ? p[i].z : p[i].w;
-                  o[i][c].x = fmaf(q, v.x, o[i][c].x);
-                  o[i][c].y = fmaf(q, v.y, o[i][c].y);
-                  o[i][c].z = fmaf(q, v.z, o[i][c].z);
-                  o[i][c].w = fmaf(q, v.w, o[i][c].w);
+                  const uint64_t q =
+                      twice(j == 0 ? p[i].x : j == 1 ? p[i].y : j == 2 ? p[i].z : p[i].w);
+                  o[i][c][0] = ptx::fma_f32x2(q, v.x, o[i][c][0]);
+                  o[i][c][1] = ptx::fma_f32x2(q, v.y, o[i][c][1]);
                 }
               }
             }
@@ -251,11 +268,9 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 0; c < DC; ++c) {
               const int col = tx * 4 + c * 64;
               if (col < d) {
-                const float4 v = *reinterpret_cast<const float4*>(Vs + n * d + col);
-                o[i][c].x = fmaf(q, v.x, o[i][c].x);
-                o[i][c].y = fmaf(q, v.y, o[i][c].y);
-                o[i][c].z = fmaf(q, v.z, o[i][c].z);
-                o[i][c].w = fmaf(q, v.w, o[i][c].w);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(Vs + n * d + col);
+                o[i][c][0] = ptx::fma_f32x2(twice(q), v.x, o[i][c][0]);
+                o[i][c][1] = ptx::fma_f32x2(twice(q), v.y, o[i][c][1]);
               }
             }
           }
@@ -276,8 +291,8 @@ __global__ void __launch_bounds__(kThreads)
           const int col = tx * 4 + c * 64;
           if (col < d)
             store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,
-                   make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv,
-                               o[i][c].w * inv));
+                   as_float4(ptx::mul_f32x2(o[i][c][0], twice(inv)),
+                             ptx::mul_f32x2(o[i][c][1], twice(inv))));
         }
         if (a.lse != nullptr && tx == 0)
           a.lse[static_cast<int64_t>(it.q0 + tok) * (a.H * a.G) + head] =
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
         const int col = tx * 4 + c * 64;
-        if (col < d) store4(slot + (col / 4 * kSlotRows + row) * 4, o[i][c]);
+        if (col < d) store4(slot + (col / 4 * kSlotRows + row) * 4, as_float4(o[i][c][0], o[i][c][1]));
       }
       if (tx == 0) {
         slot[kSlotRows * d + row] = m[i];
