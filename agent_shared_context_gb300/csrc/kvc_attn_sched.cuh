@@ -441,8 +441,9 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
 // One of `n_threads` threads joins the parts of rows [0, rows) of an item and
 // hands (row, first column, four values of O / l, lse in nats) to `store`.
 // Part p lies in slot slot_of(p) of CTA cta0 + p, `slot_rows` rows with row0
-// the first.  Parts are added in the order of their keys.
-template <typename Store>
+// the first.  Parts are added in the order of their keys; the loads of kP of them
+// are in flight at a time, which takes registers.
+template <int kP, typename Store>
 __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, int slot_rows,
                                            int row0, int d, const Item& it, int rows, int tid,
                                            int n_threads, Store store) {
@@ -456,10 +457,16 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
   for (int row = tid & (span - 1); row < rows; row += span) {
     auto part = [&](int p) { return base + (static_cast<size_t>(p) * 2 + slot_of(p)) * slot_n; };
     float M = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < it.nparts; ++p)
-      M = fmaxf(M, __ldcg(part(p) + slot_rows * d + row0 + row));
-    constexpr int kC = 4;
+    constexpr int kC = 4;                  // groups of columns at a time
+#pragma unroll 1
+    for (int p0 = 0; p0 < it.nparts; p0 += 2 * kP) {
+      float pm[2 * kP];
+#pragma unroll
+      for (int p = 0; p < 2 * kP; ++p)
+        pm[p] = p0 + p < it.nparts ? __ldcg(part(p0 + p) + slot_rows * d + row0 + row) : -INFINITY;
+#pragma unroll
+      for (int p = 0; p < 2 * kP; ++p) M = fmaxf(M, pm[p]);
+    }
 #pragma unroll 1
     for (int c0 = tid / span; c0 < d4; c0 += kC * step) {
       float4 acc[kC];
@@ -467,27 +474,35 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
 #pragma unroll
       for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int p = 0; p < it.nparts; ++p) {
-        const float* ps = part(p);
-        const float m = __ldcg(ps + slot_rows * d + row0 + row);
-        const float l = __ldcg(ps + slot_rows * d + slot_rows + row0 + row);
-        float4 v[kC];
+      for (int p0 = 0; p0 < it.nparts; p0 += kP) {
+        float pm[kP], pl[kP];
+        float4 v[kP][kC];
 #pragma unroll
-        for (int c = 0; c < kC; ++c)
-          if (c0 + c * step < d4)
-            v[c] = __ldcg(reinterpret_cast<const float4*>(ps) + (c0 + c * step) * slot_rows +
-                          row0 + row);
-        if (l == 0.f) continue;
-        const float f = part_weight(m, l, M);
-        L = fmaf(l, f, L);
+        for (int p = 0; p < kP; ++p) {
+          const float* ps = part(p0 + p);
+          const bool has = p0 + p < it.nparts;
+          pm[p] = has ? __ldcg(ps + slot_rows * d + row0 + row) : 0.f;
+          pl[p] = has ? __ldcg(ps + slot_rows * d + slot_rows + row0 + row) : 0.f;
 #pragma unroll
-        for (int c = 0; c < kC; ++c)
-          if (c0 + c * step < d4) {
-            acc[c].x = fmaf(v[c].x, f, acc[c].x);
-            acc[c].y = fmaf(v[c].y, f, acc[c].y);
-            acc[c].z = fmaf(v[c].z, f, acc[c].z);
-            acc[c].w = fmaf(v[c].w, f, acc[c].w);
-          }
+          for (int c = 0; c < kC; ++c)
+            if (has && c0 + c * step < d4)
+              v[p][c] = __ldcg(reinterpret_cast<const float4*>(ps) + (c0 + c * step) * slot_rows +
+                               row0 + row);
+        }
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          if (pl[p] == 0.f) continue;
+          const float f = part_weight(pm[p], pl[p], M);
+          L = fmaf(pl[p], f, L);
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (c0 + c * step < d4) {
+              acc[c].x = fmaf(v[p][c].x, f, acc[c].x);
+              acc[c].y = fmaf(v[p][c].y, f, acc[c].y);
+              acc[c].z = fmaf(v[p][c].z, f, acc[c].z);
+              acc[c].w = fmaf(v[p][c].w, f, acc[c].w);
+            }
+        }
       }
       const float inv = 1.f / L;
       const float lse = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;

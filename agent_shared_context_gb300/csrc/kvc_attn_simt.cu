@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads)
     if (!sh.last) continue;
     __threadfence();
     if (tid == 0) counters[it.cta0] = 0;
-    join_parts(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
+    join_parts<4>(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
                [&](int row, int col, float4 v, float lse) {
                  const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                  store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok + head * a.o_head + col,

@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!b->last[st]) continue;
       __threadfence();
       if (row == 0) counters[2 * it.cta0 + st] = 0;
-      join_parts(slots, slot_n, kSlotRows, pair ? st * kRowsM : 0, D, it, n_tok * a.G, row, 128,
+      join_parts<1>(slots, slot_n, kSlotRows, pair ? st * kRowsM : 0, D, it, n_tok * a.G, row, 128,
                  [&](int r, int col, float4 v, float lse) {
                    const int tok = r / a.G, hd = it.h * a.G + r - tok * a.G;
                    const int64_t orow = it.q0 + tok_off + tok;
