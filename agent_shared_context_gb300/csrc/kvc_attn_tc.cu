@@ -31,9 +31,10 @@
 //                   it is);
 //   warp 10         only holds its place in its warpgroup.
 //
-// A key tile is 128 rows of a page, or as many whole pages (rounded up to 8
-// rows) as fit: pages of 8, 16, 32, 64 rows fill it, others leave holes that
-// are masked.  Where a tile is not in sight of all its rows the scores are
+// A key tile is 128 keys, copied in runs that divide it and the page: pages of
+// a multiple of 16 rows fill every tile.  Of others a tile holds as many whole
+// ones (rounded up to 8 rows) as fit, or 128 rows of one, and leaves holes that
+// are masked (launch_tc says when).  Where a tile is not in sight of all its rows the scores are
 // masked, and the softmax warps look through the value rows that are not in
 // sight of all: 0 times an infinity or a NaN, which a page may hold there, is not
 // 0.  Where they find one they clear it, and if some rows do see it those add its
@@ -93,10 +94,11 @@ struct TcMaps {
 struct TcArgs {
   AttnArgs a;
   SchedArgs s;
-  FastDiv page, rows, tiles;   // by B, by page_rows, by the tiles of a group
+  FastDiv page, rows, tiles;   // by B, by run_rows, by the tiles of a group
   int32_t tok_tile;        // tokens of a row tile, floor(128 / G)
-  int32_t page_rows;       // rows of a page in a tile: B rounded up to 8, or 128
-  int32_t pages_tile;      // pages of a tile (1 if a page has 128 rows or more)
+  int32_t runs;            // a tile is copied in runs of tokens of one page,
+  int32_t run_tokens;      // so many each,
+  int32_t run_rows;        // and so many rows in shared memory
   uint32_t holes[4];       // columns of a tile that never hold a key (pages < 128 rows)
   int32_t has_holes;
   int32_t ragged;          // some tiles hold fewer than 128 keys
@@ -229,14 +231,14 @@ __device__ __forceinline__ int tile_col(const TcArgs& p, const TileSpan& t, int 
   if (rel >= t.cnt) return kTile;
   if (!p.has_holes) return rel;
   const int pg = fast_div(rel, p.page);
-  return pg * p.page_rows + (rel - pg * p.a.B);
+  return pg * p.run_rows + (rel - pg * p.a.B);
 }
 
 // Token of a key column (not of a hole).
 __device__ __forceinline__ int tile_tok(const TcArgs& p, const TileSpan& t, int col) {
   if (!p.has_holes) return t.tok0 + col;
   const int pg = fast_div(col, p.rows);
-  return t.tok0 + pg * p.a.B + (col - pg * p.page_rows);
+  return t.tok0 + pg * p.a.B + (col - pg * p.run_rows);
 }
 
 // Keys that every row of tokens [pos0, pos0 + nt) sees, and that any sees.
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
-  if (p.pages_tile * p.page_rows < kTile) {
+  if (p.runs * p.run_rows < kTile) {
     // rows that no load ever writes: 0, so that P V is 0 there
     uint4* z = reinterpret_cast<uint4*>(kv_smem);
     for (int i = threadIdx.x; i < NS * C::kSlotBytes / 16; i += kThreads)
@@ -337,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;                                    // ring % NS
     uint32_t wrap = 1;                            // parity of kv_empty[s] to wait for
     bool ok = true;
-    const int boxes = p.pages_tile * C::kSub;
-    const int my_page = lane / C::kSub, my_sub = lane - my_page * C::kSub;
-    const uint32_t tile_bytes = static_cast<uint32_t>(p.pages_tile * p.page_rows) * 128 * C::kSub;
-    uint8_t* my_dst = kv_smem + my_sub * kSubBytes + my_page * p.page_rows * 128;
+    const int boxes = p.runs * C::kSub;
+    const int my_run = lane / C::kSub, my_sub = lane - my_run * C::kSub;
+    const uint32_t tile_bytes = static_cast<uint32_t>(p.runs * p.run_rows) * 128 * C::kSub;
+    uint8_t* my_dst = kv_smem + my_sub * kSubBytes + my_run * p.run_rows * 128;
     bool bad_page = false;
 
     for (;;) {
@@ -366,21 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!more) break;
       const bool pair = it.nt > p.tok_tile;
 
-      // The pages of the lane's boxes of key tiles 0, 1, ... in order (`blk`,
-      // `sub`: page and tile in it), fetched one tile ahead.  A box beyond the pool
-      // (page P) is filled with 0.
+      // Page and first row in it of the lane's box of key tiles 0, 1, ... in order,
+      // looked up one tile ahead.  A box beyond the pool (page P) is filled with 0.
       const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
-      const int last_blk = it.kv > 0 ? fast_div(it.kv - 1, p.page) : -1;
-      const int blk_step = p.pages_tile == 1 ? 1 : p.pages_tile;
-      int blk = it.tile0 * p.pages_tile + my_page, sub = 0;
-      if (p.pages_tile == 1) {
-        blk = fast_div(it.tile0, p.tiles);
-        sub = it.tile0 - blk * p.s.group_tiles;
-      }
-      auto fetch = [&]() { return lane < boxes && blk <= last_blk ? __ldg(table + blk) : kNoPage; };
-      int ahead = fetch(), page = 0, page_before = 0;       // of the next, the last two K tiles
-      int row_k = sub * kTile, row_v = row_k;               // first row of the tile in its page
-      const int row_end = p.s.group_tiles * kTile;
+      struct Box {
+        int page, row;
+      };
+      auto fetch = [&](int tile) -> Box {
+        const int tok = tile_span(p, tile).tok0 + my_run * p.run_tokens;
+        if (lane >= boxes || tok >= it.kv) return Box{kNoPage, 0};
+        const int blk = fast_div(tok, p.page);
+        return Box{__ldg(table + blk), tok - blk * a.B};
+      };
+      Box ahead = fetch(it.tile0), now{0, 0}, before{0, 0};   // of the next, the last two K tiles
 
       // Q: one box per row tile and 64 columns
       ok = warp_wait(&b->q_empty, (n_items & 1) ^ 1, b);
@@ -402,28 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pos = 0; pos < 2 * n; ++pos) {
         // the order in which the MMAs take them: ring_k, ring_v
         const bool is_v = pos == 2 * n - 1 || (pair ? (pos & 1) : pos >= 2 && !(pos & 1));
-        int use, row;
+        Box use;
         if (is_v) {
-          use = i_v + 1 == i_k ? page : page_before;
+          use = i_v + 1 == i_k ? now : before;
           ++i_v;
-          row = row_v;
-          row_v = row + kTile == row_end ? 0 : row + kTile;
         } else {
-          page_before = page;
-          page = ahead;
-          if (++sub == p.s.group_tiles) {
-            sub = 0;
-            blk += blk_step;
-          }
-          ahead = fetch();
-          if (page < 0 || page >= a.P) {
-            bad_page |= page != kNoPage;
-            page = a.P;
-          }
-          use = page;
+          before = now;
+          now = ahead;
           ++i_k;
-          row = row_k;
-          row_k = row + kTile == row_end ? 0 : row + kTile;
+          ahead = fetch(it.tile0 + i_k);
+          if (now.page < 0 || now.page >= a.P) {
+            bad_page |= now.page != kNoPage;
+            now.page = a.P;
+          }
+          use = now;
         }
         uint64_t* bar = &b->kv_full[s];
         ok = warp_wait(&b->kv_empty[s], wrap, b);
@@ -433,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
         __syncwarp();
         if (lane < boxes)
-          tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64, row,
-                      it.h, a.layer, use);
+          tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64, use.row,
+                      it.h, a.layer, use.page);
         ++ring;
         if (++s == NS) {
           s = 0;
@@ -997,11 +989,25 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   std::memset(&p, 0, sizeof(p));
   p.a = a;
   p.tok_tile = kRowsM / a.G;
-  p.page_rows = a.B < kTile ? (a.B + 7) / 8 * 8 : kTile;
-  p.pages_tile = a.B < kTile ? kTile / p.page_rows : 1;
-  if (a.B < kTile)
+  // Where a run of 16 rows or more divides both page and tile, tiles are full whatever
+  // the page.  Otherwise a tile has whole pages, or a page whole tiles, and masked
+  // columns.  Runs of 8 rows fill them too, but their many copies cost as much as
+  // tiles of which a quarter is empty: they are taken where less than 7/8 would be
+  // filled.  (Eight chunks of 256 tokens over 8,000 keys, 32 on 8 heads of 128: full
+  // tiles by runs of 16 and more 272 us, of 8 rows 363 us; masked tiles 322 us for
+  // pages of 1,000 rows, 330 us for 40, 386 us for 200, 392 us for 48.)
+  int fit = kTile;
+  while (a.B % fit != 0) fit /= 2;
+  const int padded = (a.B + 7) / 8 * 8, tiles_page = (a.B + kTile - 1) / kTile;
+  const int filled = a.B < kTile ? kTile / padded * a.B : a.B / tiles_page;   // keys of a tile
+  const bool full = fit >= 16 || (fit == 8 && filled < kTile * 7 / 8);
+  const bool small = !full && a.B < kTile;
+  p.run_rows = full ? fit : small ? padded : kTile;
+  p.run_tokens = small ? a.B : p.run_rows;
+  p.runs = kTile / p.run_rows;
+  if (small)
     for (int n = 0; n < kTile; ++n)
-      if (n / p.page_rows >= p.pages_tile || n % p.page_rows >= a.B) p.holes[n >> 5] |= 1u << (n & 31);
+      if (n / p.run_rows >= p.runs || n % p.run_rows >= a.B) p.holes[n >> 5] |= 1u << (n & 31);
   p.has_holes = (p.holes[0] | p.holes[1] | p.holes[2] | p.holes[3]) != 0;
   SchedArgs& s = p.s;
   s.q_start = a.q_start;
@@ -1012,18 +1018,18 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   s.kv_cap = a.width * a.B;
   s.causal = a.causal;
   s.window = a.window;
-  const int group = a.B < kTile ? p.pages_tile * a.B : a.B;
+  const int group = full ? kTile : small ? p.runs * a.B : a.B;
   s.item = make_fastdiv(2 * p.tok_tile);
   s.group = make_fastdiv(group);
-  s.group_tiles = a.B < kTile ? 1 : (a.B + kTile - 1) / kTile;
-  s.tile = make_fastdiv(a.B < kTile ? group : kTile);
-  s.even = s.group_tiles == 1 || a.B % kTile == 0;
+  s.group_tiles = (group + kTile - 1) / kTile;
+  s.tile = make_fastdiv(group < kTile ? group : kTile);
+  s.even = s.group_tiles == 1;
   s.overhead = kItemCost;
   p.out32 = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) && (a.o_tok * 2) % 32 == 0 &&
             (a.o_head * 2) % 32 == 0;
-  p.ragged = p.has_holes || (a.B > kTile && a.B % kTile != 0);
+  p.ragged = p.has_holes || !s.even;
   p.page = make_fastdiv(a.B);
-  p.rows = make_fastdiv(p.page_rows);
+  p.rows = make_fastdiv(p.run_rows);
   p.tiles = make_fastdiv(s.group_tiles);
 
   TcMaps maps;
@@ -1039,9 +1045,9 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
-  e = encode_pool(&maps.k, a, 0, p.page_rows);
+  e = encode_pool(&maps.k, a, 0, p.run_rows);
   if (e != cudaSuccess) return e;
-  e = encode_pool(&maps.v, a, 1, p.page_rows);
+  e = encode_pool(&maps.v, a, 1, p.run_rows);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Cfg<D>::kSmem);
