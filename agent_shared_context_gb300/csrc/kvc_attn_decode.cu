@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
   float* join = reinterpret_cast<float*>(smem + kWarps * C::kWarpBytes);
   const int gr = lane >> 2, qc = lane & 3;         // row and pair of columns of a fragment
 
+  grid_wait();
   Walker w = walker_begin<kThreads>(p.s, &sched, a.dev_status);
   int32_t* counters = static_cast<int32_t*>(a.workspace);
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
@@ -156,8 +157,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
     // page of the lane's key of step t (-1: not to be read)
     auto page_of = [&](int t) -> int {
       const int tok = (it.tile0 + t) * kTile + warp * kKeys + lane;
-      return t < it.ntiles && lane < kKeys && tok >= any_lo && tok < any_hi ? __ldg(table + fast_div(tok, p.page))
-                                                            : -1;
+      return t < it.ntiles && lane < kKeys && tok >= any_lo && tok < any_hi
+                 ? table[fast_div(tok, p.page)]
+                 : -1;
     };
     auto issue = [&](int t, int page) {
       if (t < it.ntiles) {
@@ -495,9 +497,8 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
                            Cfg<D, NQ>::kSmem);
   if (e != cudaSuccess) return e;
   const int most = di.sm_count * (D == 128 ? 1 : 2);
-  attn_decode_kernel<D, NQ>
-      <<<most < kMaxCtas ? most : kMaxCtas, kThreads, Cfg<D, NQ>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(attn_decode_kernel<D, NQ>, dim3(most < kMaxCtas ? most : kMaxCtas), kThreads,
+                      Cfg<D, NQ>::kSmem, stream, p);
 }
 
 }  // namespace

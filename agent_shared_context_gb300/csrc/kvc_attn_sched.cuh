@@ -65,7 +65,7 @@ struct Request {
 // and keys in [0, kv_cap].
 __device__ __forceinline__ Request load_request(const SchedArgs& a, int r, bool* bad = nullptr) {
   Request q;
-  const int s0 = __ldg(a.q_start + r), s1 = __ldg(a.q_start + r + 1), n = __ldg(a.kv_lens + r);
+  const int s0 = a.q_start[r], s1 = a.q_start[r + 1], n = a.kv_lens[r];
   q.q0 = min(max(s0, 0), a.N);
   q.nq = min(max(s1, q.q0), a.N) - q.q0;
   q.kv = min(max(n, 0), a.kv_cap);

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads)
   float* Ps = Vt + ST * kTile * d;                  // [kRows][kTile + 4]
   constexpr int kPp = kTile + 4;
 
+  grid_wait();
   Walker w = walker_begin<kThreads>(sa, &sh.sched, a.dev_status);
   int32_t* counters = static_cast<int32_t*>(a.workspace);
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kAttnCounterBytes);
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads)
       int64_t off = -1;
       if (tok < it.kv) {
         const int blk = fast_div(tok, per_page);
-        const int page = __ldg(table + blk);
+        const int page = table[blk];
         if (page >= 0 && page < a.P)
           off = page * a.pool[kv].s_req + it.h * a.pool[kv].s_head +
                 static_cast<int64_t>(tok - blk * a.B) * a.pool[kv].s_tok;
@@ -364,8 +365,8 @@ cudaError_t launch_one(const AttnArgs& a, const DeviceInfo& di, cudaStream_t str
   s.overhead = 1;
   const int per_sm = 2 * (smem + sizeof(Smem) + 1024) <= static_cast<size_t>(di.smem_per_sm) ? 2 : 1;
   const int grid = di.sm_count * per_sm < kMaxCtas ? di.sm_count * per_sm : kMaxCtas;
-  fn<<<grid, kThreads, smem, stream>>>(a, s, make_fastdiv(a.B), make_fastdiv(a.d / 4));
-  return cudaGetLastError();
+  return launch_early(fn, dim3(grid), kThreads, smem, stream, a, s, make_fastdiv(a.B),
+                      make_fastdiv(a.d / 4));
 }
 
 // Two tiles where they fit in shared memory.

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       z[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
+  grid_wait();
   Walker w = walker_begin<kThreads>(p.s, &b->sched, a.dev_status);
   tc_fence_before();
   __syncthreads();
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = tile_span(p, tile).tok0 + my_run * p.run_tokens;
         if (lane >= boxes || tok >= it.kv) return Box{kNoPage, 0};
         const int blk = fast_div(tok, p.page);
-        return Box{__ldg(table + blk), tok - blk * a.B};
+        return Box{table[blk], tok - blk * a.B};
       };
       Box ahead = fetch(it.tile0), now{0, 0}, before{0, 0};   // of the next, the last two K tiles
 
@@ -1053,8 +1054,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
                            Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
-  attn_tc_kernel<D><<<grid, kThreads, Cfg<D>::kSmem, stream>>>(maps, p);
-  return cudaGetLastError();
+  return launch_early(attn_tc_kernel<D>, dim3(grid), kThreads, Cfg<D>::kSmem, stream, maps, p);
 }
 
 }  // namespace

@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int cap = a.width * a.B;                // <= 2^30
   const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  grid_wait();
   const int F = min(max(a.n_free_in[0], 0), a.P);
   auto blocks = [&](int n) { return fast_div(n + a.B - 1, page); };
 
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kWriteThreads)
                     (l * a.src[kv].s_layer + h * a.src[kv].s_head) * e;
   char* pool = static_cast<char*>(a.pool[kv].base) +
                ((a.L0 + l) * a.pool[kv].s_layer + h * a.pool[kv].s_head) * e;
+  grid_wait();
   uint4 v[kWriteVecs];
   int64_t slot[kWriteVecs];
   int col[kWriteVecs];
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kWriteThreads)
     const int64_t n = row0 + row;
     slot[k] = -1;
     if (row < rows_cta && n < a.rows) {
-      slot[k] = __ldg(a.slots + n);
+      slot[k] = a.slots[n];
       const int64_t r = BIG ? n / a.T : fast_div(static_cast<int>(n), per_src);
       v[k] = __ldcs(reinterpret_cast<const uint4*>(
           src + (r * a.src[kv].s_req + (n - r * a.T) * a.src[kv].s_tok) * e + col[k]));
@@ -314,8 +316,8 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
   int64_t grid = ((runs > a.R ? runs : a.R) + kPlanThreads - 1) / kPlanThreads;
   if (grid > di.sm_count) grid = di.sm_count;
   if (grid < 1) grid = 1;
-  fn<<<static_cast<int>(grid), kPlanThreads, smem, stream>>>(a, attn::make_fastdiv(a.B));
-  return cudaGetLastError();
+  return launch_early(fn, dim3(static_cast<unsigned>(grid)), kPlanThreads, smem, stream, a,
+                      attn::make_fastdiv(a.B));
 }
 
 cudaError_t launch_page_write(const WriteArgs& a, cudaStream_t stream) {
@@ -324,9 +326,8 @@ cudaError_t launch_page_write(const WriteArgs& a, cudaStream_t stream) {
                   static_cast<unsigned>(a.nl * a.H), 2);
   const int64_t most = int64_t(1) << 31;
   auto* fn = a.rows >= most || a.n_slots >= most ? page_write_kernel<true> : page_write_kernel<false>;
-  fn<<<grid, kWriteThreads, 0, stream>>>(a, attn::make_fastdiv(a.T), attn::make_fastdiv(a.B),
-                                         attn::make_fastdiv(a.vec_row));
-  return cudaGetLastError();
+  return launch_early(fn, grid, kWriteThreads, 0, stream, a, attn::make_fastdiv(a.T),
+                      attn::make_fastdiv(a.B), attn::make_fastdiv(a.vec_row));
 }
 
 }  // namespace kvc

@@ -2,9 +2,36 @@
 // cache (kvc_paged.cu) and its kernels.  Not part of the public ABI.
 #pragma once
 
+#include <utility>
+
 #include "kvc_internal.h"
 
 namespace kvc {
+
+// The kernels of the paged cache follow one another on a stream many times a step, and
+// most of them run for a few microseconds: each is launched while the one before it
+// ends, prepares itself and then waits for its results (grid_wait).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*fn)(P...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+}
+
+#ifdef __CUDACC__
+// Nothing that an earlier kernel may have written is read before this, and what is
+// read after it is read by ordinary loads: it was not constant since the launch.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
 
 // Requests of one kvc_page_plan call: their scans live in shared memory.
 constexpr int kMaxPlanRequests = 4096;
