@@ -12,7 +12,7 @@
 // and output of its keys.  The four warps' results are joined at the end of an
 // item.
 //
-// The mathematics is that of kvc_attn_simt.cu, P enters the product with V as
+// The mathematics is that of kvc_attn_f32.cu, P enters the product with V as
 // bf16(P) and the remainder P - bf16(P): the tensor core has time for both.
 //
 // Rows of keys beyond the request's, or out of all rows' sight, are filled with
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       if (last) {
         __threadfence();
         if (threadIdx.x == 0) counters[it.cta0] = 0;
-        join_parts<4>(slots, slot_n, kSlotRows, 0, D, it, rows, threadIdx.x, kThreads,
+        join_parts<4, 4>(slots, slot_n, kSlotRows, 0, D, it, rows, threadIdx.x, kThreads,
                    [&](int row, int col, float4 v, float lse) {
                      const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                      const int64_t orow = it.q0 + tok;

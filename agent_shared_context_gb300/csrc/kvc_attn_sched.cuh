@@ -443,7 +443,7 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
 // Part p lies in slot slot_of(p) of CTA cta0 + p, `slot_rows` rows with row0
 // the first.  Parts are added in the order of their keys; the loads of kP of them
 // are in flight at a time, which takes registers.
-template <int kP, typename Store>
+template <int kP, int kC, typename Store>
 __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, int slot_rows,
                                            int row0, int d, const Item& it, int rows, int tid,
                                            int n_threads, Store store) {
@@ -457,7 +457,6 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
   for (int row = tid & (span - 1); row < rows; row += span) {
     auto part = [&](int p) { return base + (static_cast<size_t>(p) * 2 + slot_of(p)) * slot_n; };
     float M = -INFINITY;
-    constexpr int kC = 4;                  // groups of columns at a time
 #pragma unroll 1
     for (int p0 = 0; p0 < it.nparts; p0 += 2 * kP) {
       float pm[2 * kP];

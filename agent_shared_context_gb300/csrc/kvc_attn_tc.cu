@@ -1,7 +1,7 @@
 // kvc_attn_tc.cu -- attention of a chunk of new tokens over a paged cache on
 // tcgen05 tensor cores (bf16, d = 64 or 128).
 //
-// The mathematics is that of kvc_attn_simt.cu: one pass over the keys with the
+// The mathematics is that of kvc_attn_f32.cu: one pass over the keys with the
 // running maximum m and sum l of each row's softmax.  Any reference value that
 // keeps exp2(x - m) in range gives the same O / l, so m follows the maximum
 // only when a tile raises it by more than 8 (log2): P then stays below 2^8,
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!b->last[st]) continue;
       __threadfence();
       if (row == 0) counters[2 * it.cta0 + st] = 0;
-      join_parts<1>(slots, slot_n, kSlotRows, pair ? st * kRowsM : 0, D, it, n_tok * a.G, row, 128,
+      join_parts<1, 4>(slots, slot_n, kSlotRows, pair ? st * kRowsM : 0, D, it, n_tok * a.G, row, 128,
                  [&](int r, int col, float4 v, float lse) {
                    const int tok = r / a.G, hd = it.h * a.G + r - tok * a.G;
                    const int64_t orow = it.q0 + tok_off + tok;

@@ -148,7 +148,7 @@ Span rows_span(const kvc_paged* pg, const kvc_attn_params* at, const void* p, in
 }
 
 size_t attn_workspace_bytes(const kvc_paged* pg) {
-  return pg->dtype == KVC_BF16 ? attn_tc_workspace_bytes(pg->d) : attn_simt_workspace_bytes(pg->d);
+  return pg->dtype == KVC_BF16 ? attn_tc_workspace_bytes(pg->d) : attn_f32_workspace_bytes(pg->d);
 }
 
 }  // namespace
@@ -354,7 +354,7 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
   a.scale_log2 = at->scale * 1.4426950408889634f;
   a.workspace = workspace;
   a.dev_status = dev_status;
-  const cudaError_t e = pg->dtype == KVC_F32    ? launch_attn_simt(a, stream)
+  const cudaError_t e = pg->dtype == KVC_F32    ? launch_attn_f32(a, stream)
                         : attn_decode_fits(a) ? launch_attn_decode(a, stream)
                                               : launch_attn_tc(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvc_paged_attention launch");

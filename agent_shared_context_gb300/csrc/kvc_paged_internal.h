@@ -82,8 +82,8 @@ struct AttnArgs {
 // Bytes of the workspace: arrival counters (zero between calls), then the
 // partial rows of divided items.
 constexpr size_t kAttnCounterBytes = 8192;
-size_t attn_simt_workspace_bytes(int d);   // f32
-cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t stream);
+size_t attn_f32_workspace_bytes(int d);   // f32
+cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t stream);
 size_t attn_tc_workspace_bytes(int d);     // bf16, d = 64 or 128
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream);
 // bf16, decoding; its workspace is part of the one above.
