@@ -8,31 +8,36 @@
 // key keeps m = -inf, l = 0 and gives out = 0, lse = -inf.
 //
 // Both products run on the tensor cores with each f32 factor as the sum of two
-// tf32 numbers (11 bits each): x = h + e, h = tf32(x), e = tf32(x - h), and
-// x y = h h' + h e' + e h' up to 3 2^-22 |x y|.  The tensor core's sums may drop
-// bits where an FMA would round, so no sum there is longer than a tile: a tile's
-// P V is added to O by an FMA.  (Below 2^-115, e loses bits of its own.)  FP32
-// FMAs, the plain way, are bound by their rate and by shared memory: they took
-// 338 us where this takes FIG_G us (4 requests, 300 tokens each, 4,000 keys, 8 on
-// 2 heads of 64), and 199 us where this takes FIG_J us (decoding, 16 requests of
-// 5,000 keys, heads of 128: 164 MB).
+// tf32 numbers of 11 bits: x = h + e with h = tf32(x) rounded and e = x - h cut,
+// and x y = h h' + h e' + e h' up to 5 2^-22 |x y| (the cut 2^-21 of each, and
+// e e').  The tensor core's sums may drop bits where an FMA would round, so no
+// sum of theirs is longer than a tile: a tile's P V is added to O by an FMA.
+// Numbers below 2^-115 keep the 11 bits of h alone.
 //
 // A row is (token, query head of the KV head's group), so that K and V are read
-// once for the whole group.  Eight warps: RB blocks of 16 rows times 8 / RB runs
-// of the tile's keys.  A warp keeps m, l and O of its rows and keys by itself; the
-// runs are joined at the end of an item.  The order of the columns of d in the
-// first product and of the keys in the second is free, as long as both factors
-// have the same: a lane takes four consecutive columns of a key for two steps of
-// 8, and the scores it has are the factors of P V that it needs.  Units of 16
-// bytes are placed so that the lanes of a load are in banks of their own.
-//
-// The splitting of K and V falls to every block of 16 rows anew; it costs about
-// as much time as the products and runs beside them.  The next tiles are copied
-// (cp.async) while one is worked on.
+// once for the whole group.  Eight warps: RB groups of rows, of MB blocks of 16,
+// times 8 / RB runs of the tile's keys.  A warp keeps m, l and O of its rows and
+// keys by itself; the runs are joined at the end of an item.  The order of the
+// columns of d in the first product and of the keys in the second is free as long
+// as both factors have the same one: a lane takes four consecutive columns of a
+// key for two steps of 8, and the scores that it has are the factors of P V that
+// it needs.  Units of 16 bytes are placed so that the lanes of a load are in banks
+// of their own.  The next tiles are copied (cp.async) while one is worked on.
 //
 // An infinity or a NaN cannot be split, and a key out of a row's sight must add
 // nothing even if its values are infinite: a tile that has one is worked through
 // element by element in FP32.
+//
+// Measured, in us, with FP32 FMAs in place of the tensor cores in brackets: four
+// chunks of 300 tokens over 4,000 keys, 8 on 2 heads, of 64: 236 (338), 40 TFLOP/s
+// of the 9.5 GFLOP that count; of 128: 420 (685); decoding 16 requests of 5,000
+// keys with heads of 128: 71 (199), 2.3 TB/s; six ragged chunks of up to 65 tokens
+// over 2,000 keys, heads of 64: 29 (41).  (FMAs were bound by their rate and by
+// shared memory.)  The tensor cores alone would take 95 us for the first: there is
+// room for two warps a scheduler, 255 registers each, and they wait for one
+// another's chains (issue slots 43%, tensor pipe 40% busy).  Two blocks of 16 rows
+// in a warp share the splitting of K and V: with one block, 16 warps an SM, the
+// first took 271 us.
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
 
@@ -111,7 +116,7 @@ constexpr float kTooLarge = 3.39e38f;      // h might be infinite
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
       " {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DC, RB, MB>::kCtasSm)
     if (!sh.last) continue;
     __threadfence();
     if (tid == 0) counters[it.cta0] = 0;
-    join_parts<4, 2>(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
+    join_parts<4, DC * MB <= 4 && C::kCtasSm == 1 ? 4 : 2>(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
                   [&](int row, int col, float4 v, float lse) {
                     const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                     store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok +
@@ -605,7 +610,8 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
                       make_fastdiv(a.B));
 }
 
-// 16 rows where the requests have no more on average.
+// 16 rows where the requests have no more on average: 64 would be idle for the most
+// part (decoding as above 124 us with them).
 template <int DC>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   if (a.G <= 16 && static_cast<int64_t>(a.N) * a.G <= static_cast<int64_t>(a.R) * 16)
