@@ -505,7 +505,15 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
 
 // At most one new token per request on average, all query heads of a KV head in
 // one row tile.
-bool attn_decode_fits(const AttnArgs& a) { return a.N <= a.R && a.G <= 16; }
+// No more tokens than requests, and few: the host does not know the lengths, and one
+// request may have all of the tokens, which then read its keys once for each 8 or 16
+// rows.  With 32 query heads on 8 of 128, decoding here against the chunk kernel: 2
+// requests of 1,000 keys 11.9 us (23.6), 16 of 4,000 54 (59), 32 of 1,000 38 (44), 64 of
+// 4,000 181 (179); all tokens one request's, 10,240 keys: 8 of them 40 us (48), 16 65
+// (50), 32 114 (52), 64 214 (61).
+bool attn_decode_fits(const AttnArgs& a) {
+  return a.N <= a.R && a.G <= 16 && static_cast<int64_t>(a.N) * a.G <= 128;
+}
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
   if (a.d == 128)

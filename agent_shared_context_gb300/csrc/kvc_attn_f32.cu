@@ -610,11 +610,13 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t stream) {
                       make_fastdiv(a.B));
 }
 
-// 16 rows where the requests have no more on average: 64 would be idle for the most
-// part (decoding as above 124 us with them).
+// 16 rows where the requests have no more on average, since 64 would be idle for the
+// most part (decoding as above 124 us with them); not beyond 256 in all, which could be
+// one request's and would read its keys 16 times.
 template <int DC>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
-  if (a.G <= 16 && static_cast<int64_t>(a.N) * a.G <= static_cast<int64_t>(a.R) * 16)
+  const int64_t rows = static_cast<int64_t>(a.N) * a.G;
+  if (a.G <= 16 && rows <= static_cast<int64_t>(a.R) * 16 && rows <= 256)
     return launch_one<DC, 1, 1>(a, stream);
   return launch_one<DC, 2, 2>(a, stream);
 }

@@ -521,3 +521,81 @@ def test_write_into_token_major_pools():
     for x, s in ((K, src[0]), (V, src[1])):
         want = PO.page_write(s.float().cpu().numpy(), slots.cpu().numpy(), np.zeros(x.shape), 0)
         assert np.array_equal(x.float().cpu().numpy(), want)
+
+
+FEW = [(1, 1), (1, 300), (0, 7), (2, 1030), (0, 0), (1, 128)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [2, 9, 12, 16])
+def test_decode_few_requests_head_groups(d, G):
+    b = Batch(FEW, 2 * G, 2, d, 20, "bf16", seed=G)
+    b.run()
+    b.check()
+
+
+def test_decode_thirty_tokens_of_one_request():
+    b = Batch([(30, 500)] + [(0, 9)] * 40, 8, 2, 128, 16, "bf16", seed=2)
+    b.run()
+    b.check()
+
+
+@pytest.mark.parametrize("d", [4, 20, 64, 80, 96, 128, 132, 256])
+@pytest.mark.parametrize("G", [1, 3, 16])
+def test_f32_decode(d, G):
+    b = Batch(FEW + [(1, 700)], 2 * G, 2, d, 17, "f32", seed=d + G)
+    b.run()
+    b.check()
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 1), (True, 50), (True, 200)])
+def test_f32_decode_masks(causal, window):
+    b = Batch(FEW, 8, 2, 64, 16, "f32", seed=window)
+    b.run(causal, window)
+    b.check(causal, window)
+
+
+@pytest.mark.parametrize("lens", [FEW, [(40, 200), (1, 77), (130, 131)]])
+@pytest.mark.parametrize("d", [64, 128, 192])
+@pytest.mark.parametrize("where", ["K", "V", "q"])
+def test_f32_infinities_in_sight(lens, d, where):
+    """Rows that see an infinite value (or a value near the type's largest) get what
+    the formula says; the rest what they got before."""
+    b = Batch(lens, 4, 2, d, 16, "f32", seed=6)
+    at = (b.table[1, 0], 0, 0, 0) if where != "q" else (int(b.q_start[1]), 0)
+    x = {"K": b.K, "V": b.V, "q": b.q}[where]
+    x[at][d - 1] = float("inf")
+    b.run()
+    torch.cuda.synchronize()
+    r0, r1 = int(b.q_start[1]), int(b.q_start[2])
+    heads = slice(0, 1) if where == "q" else slice(0, 2)
+    if where == "K":                              # a score of -inf has no weight, +inf no softmax
+        up = b.q[r0:r1, :2, d - 1] > 0
+        assert torch.equal(b.out[r0:r1, :2].isnan().all(-1), up)
+        assert torch.equal(b.out[r0:r1, :2].isfinite().all(-1), ~up)
+    else:
+        assert not b.out[r0:r1, heads].isfinite().all()
+    if where == "V":                              # only the last column of the first KV head
+        assert b.out[r0:r1, :2, :d - 1].isfinite().all()
+        assert (b.out[r0:r1, :2, d - 1] == float("inf")).all()
+    # what does not see it is as it would be without
+    x[at][d - 1] = 3.4e38 if where == "V" else 0.5
+    hx = {"K": b.host[0], "V": b.host[1], "q": b.host[2]}[where]
+    hx[at][d - 1] = 3.4e38 if where == "V" else 0.5
+    got = b.out.clone()
+    b.run()
+    b.check()
+    torch.cuda.synchronize()
+    same = torch.ones(b.N, 4, dtype=torch.bool)
+    same[r0:r1, heads] = False
+    assert torch.allclose(got[same.cuda()], b.out[same.cuda()], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("lens", [FEW, [(40, 200), (1, 77), (130, 131)]])
+def test_f32_large_and_small_numbers(lens):
+    b = Batch(lens, 4, 2, 64, 16, "f32", seed=8)
+    for x, h, f in ((b.K, b.host[0], 1e18), (b.V, b.host[1], 1e30), (b.q, b.host[2], 1e-18)):
+        h.mul_(f)
+        x.copy_(h)
+    b.run()
+    b.check()
