@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DC, RB, MB>::kCtasSm)
     if (!sh.last) continue;
     __threadfence();
     if (tid == 0) counters[it.cta0] = 0;
-    join_parts<4, DC * MB <= 4 && C::kCtasSm == 1 ? 4 : 2>(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
+    constexpr int kWide = DC * MB <= 4 && C::kCtasSm == 1 ? 4 : 2;   // as registers allow
+    join_parts<4, kWide>(slots, slot_n, kSlotRows, 0, d, it, rows, tid, kThreads,
                   [&](int row, int col, float4 v, float lse) {
                     const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                     store4(static_cast<float*>(a.out) + (it.q0 + tok) * a.o_tok +

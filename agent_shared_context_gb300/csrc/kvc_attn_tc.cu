@@ -47,6 +47,17 @@
 // single mode, which waits for memory anyway): few steps of a long context.  S
 // leaves room for it in TMEM, beside P.
 //
+// Measured: dense prefill of two contexts of 8,192 tokens, 32 query heads on 8 of 128,
+// 1.0 ms, 1.1 PFLOP/s or 0.58 of the library's matrix products; sixteen chunks of 128
+// tokens over 10,368 keys 325 us, 1.05 PFLOP/s; five ragged ones of up to 700 tokens,
+// 28 on 4 heads, a window of 4,096, pages of 48: 108 us, 0.57 PFLOP/s.  A pair of row
+// tiles takes some 3,800 cycles per 128 keys, of which the MMAs need 2,500: with both
+// operands of S = Q K^T in shared memory (TMEM is full: S and O of two streams) a step
+// of 16 columns takes 90 cycles instead of 64 for reading them, and each half of a tile
+// waits for the softmax's and the MMA's signals.  An item costs some 10,000 cycles
+// besides (masked tiles, the output), a CTA 5 us to its first tile, a divided item's
+// end 8 us.
+//
 // Every wait is bounded: one that expires stores KVC_ERR_DEVICE_TIMEOUT into
 // *dev_status and raises the CTA's abort flag; the roles stop, copies and MMAs
 // in flight are waited for (with the limit again), TMEM is freed.

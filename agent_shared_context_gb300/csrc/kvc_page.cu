@@ -16,7 +16,10 @@
 // those that it writes, so repeating the call repeats its result.
 //
 // Bound by launch and L2 latency for a step of a few requests, by the 12 bytes
-// written per token for large admissions.
+// written per token for large admissions.  Measured: 16 requests with a token each
+// 5.4 us, most of it the host's; 1,024 requests of which 100 end and the rest bring
+// up to 1,024 tokens each, 465,000 in all, 9.0 us (5.8 MB: 0.86 us of HBM time; the
+// sums over the requests and the search of each run of tokens are the rest).
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
 
@@ -250,7 +253,9 @@ constexpr int kWriteVecs = 4;                    // vectors per thread, all in f
 // One CTA copies a run of rows of one (layer, head) of K or V.  Bound by HBM:
 // each 16-byte vector is read once and written once, past the caches.  BIG: row
 // or slot numbers beyond 31 bits (64-bit divisions made the copy wait for
-// arithmetic: two trajectories of 10,240 tokens took 1,051 us with them).
+// arithmetic: two trajectories of 10,240 tokens took 1,051 us with them; they take
+// 746 us now, 5.37 GB at 7.2 TB/s, 1.06 of a device copy's rate).  A step's rows of
+// one layer, 16 tokens or 2,048, take 8 to 9 us, most of it the host's.
 template <bool BIG>
 __global__ void __launch_bounds__(kWriteThreads)
     page_write_kernel(const WriteArgs a, const FastDiv per_src, const FastDiv per_page,

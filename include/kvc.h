@@ -513,9 +513,13 @@ typedef struct kvc_attn_params {
  * A row that sees no key gets out = 0 and lse = -inf.  Key and value rows at
  * or beyond kv_lens[r] are never used, whatever they hold.  n == 1 is
  * decoding; requests with one token, with many and with none may be mixed.
- * Rows of no request are not written.  bf16 runs on tcgen05 tensor cores
- * with fp32 softmax and accumulation (the probabilities are rounded to bf16
- * for the product with V); f32 runs on FP32 FMA.
+ * Rows of no request are not written.  All sums, maxima and the softmax
+ * are fp32.  bf16: chunks run on tcgen05 tensor cores, with the probabilities
+ * rounded to bf16 for the product with V and the remainder of those that carry
+ * much of their row multiplied too; up to 128 rows of no more tokens than
+ * requests run in a decoding kernel on warp-level tensor-core instructions.
+ * f32 runs on these with every factor split into two tf32 numbers: 21 bits or
+ * more of each product are kept (11 for factors below 2^-115).
  *
  * `workspace` holds kvc_paged_attention_workspace() bytes (0 for descriptors
  * that the call would refuse), 256-byte aligned.  ITS FIRST 8,192 BYTES MUST
