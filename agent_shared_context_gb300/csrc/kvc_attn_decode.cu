@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
       if (last) {
         __threadfence();
         if (threadIdx.x == 0) counters[it.cta0] = 0;
-        join_parts<4, 4>(slots, slot_n, kSlotRows, 0, D, it, rows, threadIdx.x, kThreads,
+        join_parts<8, 1>(slots, slot_n, kSlotRows, 0, D, it, rows, threadIdx.x, kThreads,
                    [&](int row, int col, float4 v, float lse) {
                      const int tok = row / a.G, head = it.h * a.G + row - tok * a.G;
                      const int64_t orow = it.q0 + tok;

@@ -450,6 +450,20 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return l == 0.0f ? 0.0f : exp2f(m - M);
 }
 
+__device__ __forceinline__ void scale(float4& x, float f) {
+  x.x *= f;
+  x.y *= f;
+  x.z *= f;
+  x.w *= f;
+}
+
+__device__ __forceinline__ void add_scaled(float4& x, float4 v, float f) {
+  x.x = fmaf(v.x, f, x.x);
+  x.y = fmaf(v.y, f, x.y);
+  x.z = fmaf(v.z, f, x.z);
+  x.w = fmaf(v.w, f, x.w);
+}
+
 // One of `n_threads` threads joins the parts of rows [0, rows) of an item and
 // hands (row, first column, four values of O / l, lse in nats) to `store`.
 // Part p lies in slot slot_of(p) of CTA cta0 + p, `slot_rows` rows with row0
@@ -468,20 +482,10 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
 #pragma unroll 1
   for (int row = tid & (span - 1); row < rows; row += span) {
     auto part = [&](int p) { return base + (static_cast<size_t>(p) * 2 + slot_of(p)) * slot_n; };
-    float M = -INFINITY;
-#pragma unroll 1
-    for (int p0 = 0; p0 < it.nparts; p0 += 2 * kP) {
-      float pm[2 * kP];
-#pragma unroll
-      for (int p = 0; p < 2 * kP; ++p)
-        pm[p] = p0 + p < it.nparts ? __ldcg(part(p0 + p) + slot_rows * d + row0 + row) : -INFINITY;
-#pragma unroll
-      for (int p = 0; p < 2 * kP; ++p) M = fmaxf(M, pm[p]);
-    }
 #pragma unroll 1
     for (int c0 = tid / span; c0 < d4; c0 += kC * step) {
       float4 acc[kC];
-      float L = 0.f;
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -492,7 +496,7 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
         for (int p = 0; p < kP; ++p) {
           const float* ps = part(p0 + p);
           const bool has = p0 + p < it.nparts;
-          pm[p] = has ? __ldcg(ps + slot_rows * d + row0 + row) : 0.f;
+          pm[p] = has ? __ldcg(ps + slot_rows * d + row0 + row) : -INFINITY;
           pl[p] = has ? __ldcg(ps + slot_rows * d + slot_rows + row0 + row) : 0.f;
 #pragma unroll
           for (int c = 0; c < kC; ++c)
@@ -500,6 +504,14 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
               v[p][c] = __ldcg(reinterpret_cast<const float4*>(ps) + (c0 + c * step) * slot_rows +
                                row0 + row);
         }
+        float top = M;
+#pragma unroll
+        for (int p = 0; p < kP; ++p) top = fmaxf(top, pm[p]);
+        const float f0 = part_weight(M, L, top);
+        M = top;
+        L *= f0;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) scale(acc[c], f0);
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
           if (pl[p] == 0.f) continue;
@@ -507,12 +519,7 @@ __device__ __forceinline__ void join_parts(const float* slots, size_t slot_n, in
           L = fmaf(pl[p], f, L);
 #pragma unroll
           for (int c = 0; c < kC; ++c)
-            if (c0 + c * step < d4) {
-              acc[c].x = fmaf(v[p][c].x, f, acc[c].x);
-              acc[c].y = fmaf(v[p][c].y, f, acc[c].y);
-              acc[c].z = fmaf(v[p][c].z, f, acc[c].z);
-              acc[c].w = fmaf(v[p][c].w, f, acc[c].w);
-            }
+            if (c0 + c * step < d4) add_scaled(acc[c], v[p][c], f);
         }
       }
       const float inv = 1.f / L;

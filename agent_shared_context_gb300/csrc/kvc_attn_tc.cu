@@ -284,15 +284,13 @@ template <int D, int kC, int kP>
 __device__ __forceinline__ void join_row(const float* slots, size_t slot_n, int nparts, int row,
                                          __nv_bfloat16* out, bool out32, float* lse) {
   auto part = [&](int n) { return slots + (static_cast<size_t>(n) * 2 + slot_of(n)) * slot_n; };
-  float M = -INFINITY;
-#pragma unroll 2
-  for (int n = 0; n < nparts; ++n) M = fmaxf(M, __ldcg(part(n) + kSlotRows * D + row));
-  float L = 0.f;
+  float M = -INFINITY, L = 0.f;
 #pragma unroll 1
   for (int c0 = 0; c0 < D / 4; c0 += kC) {
     float4 acc[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    M = -INFINITY;
     L = 0.f;
 #pragma unroll 1
     for (int n0 = 0; n0 < nparts; n0 += kP) {
@@ -307,18 +305,21 @@ __device__ __forceinline__ void join_row(const float* slots, size_t slot_n, int 
 #pragma unroll
         for (int c = 0; c < kC; ++c) v[n][c] = __ldcg(o + c * kSlotRows);
       }
+      float top = M;
+#pragma unroll
+      for (int n = 0; n < kP; ++n) top = fmaxf(top, pm[n]);
+      const float f0 = part_weight(M, L, top);
+      M = top;
+      L *= f0;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) scale(acc[c], f0);
 #pragma unroll
       for (int n = 0; n < kP; ++n) {
         if (pl[n] == 0.f) continue;              // nothing seen, or no such part
         const float f = part_weight(pm[n], pl[n], M);
         L = fmaf(pl[n], f, L);
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          acc[c].x = fmaf(v[n][c].x, f, acc[c].x);
-          acc[c].y = fmaf(v[n][c].y, f, acc[c].y);
-          acc[c].z = fmaf(v[n][c].z, f, acc[c].z);
-          acc[c].w = fmaf(v[n][c].w, f, acc[c].w);
-        }
+        for (int c = 0; c < kC; ++c) add_scaled(acc[c], v[n][c], f);
       }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
