@@ -395,9 +395,7 @@ def kvc_selftest_bounded_wait(max_polls: int, dev_status: Ptr, stream=None,
 
 
 def _v(x) -> kvc_cache_view:
-    if isinstance(x, kvc_cache_view):
-        return x
-    return cache_view(x)
+    return x if type(x) is kvc_cache_view else cache_view(x)
 
 
 # ---------------------------------------------------------------- paged caches
@@ -443,7 +441,10 @@ def kvc_page_write(pg: kvc_paged, src_K, src_V, slot_map: Ptr, pool_K, pool_V, l
     """Rows of ``src_K`` / ``src_V`` [n_src, n_layers, H, T, d] into the slots
     ``slot_map`` [n_src, T] of layers ``layer`` .. of the pools.  Raw views
     need ``shape`` = (n_src, n_layers, T)."""
-    n, nl, T = shape if shape is not None else (src_K.shape[0], src_K.shape[1], src_K.shape[3])
+    if shape is not None:
+        n, nl, T = shape
+    else:
+        n, nl, _, T, _ = src_K.shape
     st = lib.kvc_page_write(ctypes.byref(pg), n, T, layer, nl, _v(src_K), _v(src_V),
                             _addr(slot_map), _v(pool_K), _v(pool_V), _stream(stream))
     return _done(st, "kvc_page_write", check)
