@@ -722,18 +722,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto odd = [](uint32_t u) {                       // an exponent of all ones
             return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
           };
-#pragma unroll 2
+          // 0 times each is 0, or NaN
+          uint32_t z0 = 0, z1 = 0;
+#pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             int n;
-            uint4* q = at(j, &n);
-            if (n >= c1 && n < c2) continue;
-            const uint4 v = *q;
-            if (!(odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w))) continue;
-            if (n >= c0 && n < c3) {
-              atomicOr(&b->poison[slot_v][n >> 5], 1u << (n & 31));
-            } else {
-              *q = make_uint4(0, 0, 0, 0);                  // no row sees it
-              fence_proxy_async_smem();
+            const uint4 v = *at(j, &n);
+            z0 = fma_bf16x2(v.x, 0, z0);
+            z1 = fma_bf16x2(v.y, 0, z1);
+            z0 = fma_bf16x2(v.z, 0, z0);
+            z1 = fma_bf16x2(v.w, 0, z1);
+          }
+          if ((z0 | z1) != 0) {
+#pragma unroll 1
+            for (int j = 0; j < D / 16; ++j) {
+              int n;
+              uint4* q = at(j, &n);
+              if (n >= c1 && n < c2) continue;
+              const uint4 v = *q;
+              if (!(odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w))) continue;
+              if (n >= c0 && n < c3) {
+                atomicOr(&b->poison[slot_v][n >> 5], 1u << (n & 31));
+              } else {
+                *q = make_uint4(0, 0, 0, 0);                  // no row sees it
+                fence_proxy_async_smem();
+              }
             }
           }
           ok = meet();

@@ -320,6 +320,13 @@ __device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
                : "memory");
 }
 
+// a b + c of two bf16 each.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // --------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
   uint64_t d;
