@@ -711,59 +711,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Sight see = sight(a, it.kv, it.pos0, it.nt);
           const int c0 = tile_col(p, t, see.any_lo), c3 = tile_col(p, t, see.any_hi);
           const int c1 = tile_col(p, t, see.all_lo), c2 = tile_col(p, t, see.all_hi);
-          uint8_t* rows = kv_smem + slot_v * C::kSlotBytes + half * kHalf * 128;
-          // 16 bytes at a time, neighbouring threads neighbouring bytes
-          auto at = [&](int j, int* n) {
-            const int u = row + 128 * j;
-            *n = half * kHalf + ((u >> 3) & (kHalf - 1));
-            return reinterpret_cast<uint4*>(rows + (u / (8 * kHalf)) * kSubBytes +
-                                            ((u >> 3) & (kHalf - 1)) * 128 + (u & 7) * 16);
-          };
-          auto odd = [](uint32_t u) {                       // an exponent of all ones
-            return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-          };
-          // 0 times each is 0, or NaN
-          uint32_t z0 = 0, z1 = 0;
+          if (half * kHalf < c1 || half * kHalf + kHalf > c2) {   // not seen by all rows
+            uint8_t* rows = kv_smem + slot_v * C::kSlotBytes + half * kHalf * 128;
+            // 16 bytes at a time, neighbouring threads neighbouring bytes
+            auto at = [&](int j, int* n) {
+              const int u = row + 128 * j;
+              *n = half * kHalf + ((u >> 3) & (kHalf - 1));
+              return reinterpret_cast<uint4*>(rows + (u / (8 * kHalf)) * kSubBytes +
+                                              ((u >> 3) & (kHalf - 1)) * 128 + (u & 7) * 16);
+            };
+            auto odd = [](uint32_t u) {                       // an exponent of all ones
+              return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+            };
+            // 0 times each is 0, or NaN
+            uint32_t z0 = 0, z1 = 0;
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            int n;
-            const uint4 v = *at(j, &n);
-            z0 = fma_bf16x2(v.x, 0, z0);
-            z1 = fma_bf16x2(v.y, 0, z1);
-            z0 = fma_bf16x2(v.z, 0, z0);
-            z1 = fma_bf16x2(v.w, 0, z1);
-          }
-          if ((z0 | z1) != 0) {
-#pragma unroll 1
             for (int j = 0; j < D / 16; ++j) {
               int n;
-              uint4* q = at(j, &n);
-              if (n >= c1 && n < c2) continue;
-              const uint4 v = *q;
-              if (!(odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w))) continue;
-              if (n >= c0 && n < c3) {
-                atomicOr(&b->poison[slot_v][n >> 5], 1u << (n & 31));
-              } else {
-                *q = make_uint4(0, 0, 0, 0);                  // no row sees it
-                fence_proxy_async_smem();
+              const uint4 v = *at(j, &n);
+              z0 = fma_bf16x2(v.x, 0, z0);
+              z1 = fma_bf16x2(v.y, 0, z1);
+              z0 = fma_bf16x2(v.z, 0, z0);
+              z1 = fma_bf16x2(v.w, 0, z1);
+            }
+            if ((z0 | z1) != 0) {
+#pragma unroll 1
+              for (int j = 0; j < D / 16; ++j) {
+                int n;
+                uint4* q = at(j, &n);
+                if (n >= c1 && n < c2) continue;
+                const uint4 v = *q;
+                if (!(odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w))) continue;
+                if (n >= c0 && n < c3) {
+                  atomicOr(&b->poison[slot_v][n >> 5], 1u << (n & 31));
+                } else {
+                  *q = make_uint4(0, 0, 0, 0);                  // no row sees it
+                  fence_proxy_async_smem();
+                }
               }
             }
-          }
-          ok = meet();
-          if (!ok) break;
-          bad = &b->poison[slot_v][2 * half];
-          if ((bad[0] | bad[1]) != 0) {
-#pragma unroll 1
-            for (int j = 0; j < D / 16; ++j) {
-              int n;
-              uint4* q = at(j, &n);
-              if ((bad[(n >> 5) & 1] >> (n & 31)) & 1u) *q = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
             ok = meet();
             if (!ok) break;
-          } else {
-            bad = nullptr;
+            bad = &b->poison[slot_v][2 * half];
+            if ((bad[0] | bad[1]) != 0) {
+#pragma unroll 1
+              for (int j = 0; j < D / 16; ++j) {
+                int n;
+                uint4* q = at(j, &n);
+                if ((bad[(n >> 5) & 1] >> (n & 31)) & 1u) *q = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              ok = meet();
+              if (!ok) break;
+            } else {
+              bad = nullptr;
+            }
           }
         }
         ok = warp_wait(&b->s_full[st][half], ph_s, b);
