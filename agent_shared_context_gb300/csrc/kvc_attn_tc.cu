@@ -791,9 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 2; ++c) {
               const uint32_t keep = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) &
                                     ~(half == 0 ? p.holes[c] : p.holes[2 + c]);
+              if (__any_sync(0xffffffffu, keep != 0xffffffffu)) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((keep >> j) & 1u)) x[32 * c + j] = 0xff800000u;      // -inf
+                for (int j = 0; j < 32; ++j)
+                  if (!((keep >> j) & 1u)) x[32 * c + j] = 0xff800000u;    // -inf
+              }
             }
           }
           auto sc = [&](int j) { return __uint_as_float(x[j]); };
