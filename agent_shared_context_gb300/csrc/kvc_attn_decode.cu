@@ -23,10 +23,10 @@
 //
 // The work is divided over a persistent grid as kvc_attn_sched.cuh says.
 //
-// Measured, 32 query heads on 8 of 128: 16 requests of 10,240 keys 110 us, 671 MB at
-// 6.1 TB/s (asymptotically 7.2 TB/s and some 12 us of launch, division of the work,
-// first loads and joining); one request of 131,072 keys 91 us, 5.9 TB/s; one of 777
-// keys 10.2 us, all of it latency.  Where the chunk kernel would be faster: launch
+// Measured, 32 query heads on 8 of 128: 16 requests of 10,240 keys 109 us, 671 MB at
+// 6.2 TB/s (asymptotically 7.2 TB/s and some 10 us of launch, division of the work,
+// first loads and joining); one request of 131,072 keys 88 us, 6.1 TB/s; one of 777
+// keys 9.5 us, all of it latency.  Where the chunk kernel would be faster: launch
 // rules below.
 #include <cuda_bf16.h>
 

@@ -32,7 +32,7 @@
 // chunks of 300 tokens over 4,000 keys, 8 on 2 heads, of 64: 236 (338), 40 TFLOP/s
 // of the 9.5 GFLOP that count; of 128: 420 (685); decoding 16 requests of 5,000
 // keys with heads of 128: 71 (199), 2.3 TB/s; six ragged chunks of up to 65 tokens
-// over 2,000 keys, heads of 64: 29 (41).  (FMAs were bound by their rate and by
+// over 2,000 keys, heads of 64: 28 (41).  (FMAs were bound by their rate and by
 // shared memory.)  The tensor cores alone would take 95 us for the first: there is
 // room for two warps a scheduler, 255 registers each, and they wait for one
 // another's chains (issue slots 43%, tensor pipe 40% busy).  Two blocks of 16 rows

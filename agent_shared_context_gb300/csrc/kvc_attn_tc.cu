@@ -48,9 +48,9 @@
 // leaves room for it in TMEM, beside P.
 //
 // Measured: dense prefill of two contexts of 8,192 tokens, 32 query heads on 8 of 128,
-// 1.0 ms, 1.1 PFLOP/s or 0.58 of the library's matrix products; sixteen chunks of 128
-// tokens over 10,368 keys 325 us, 1.05 PFLOP/s; five ragged ones of up to 700 tokens,
-// 28 on 4 heads, a window of 4,096, pages of 48: 108 us, 0.57 PFLOP/s.  A pair of row
+// 0.97 ms, 1.14 PFLOP/s or 0.60 of the library's matrix products; sixteen chunks of 128
+// tokens over 10,368 keys 320 us, 1.08 PFLOP/s; five ragged ones of up to 700 tokens,
+// 28 on 4 heads, a window of 4,096, pages of 48: 105 us, 0.59 PFLOP/s.  A pair of row
 // tiles takes some 3,800 cycles per 128 keys, of which the MMAs need 2,500: with both
 // operands of S = Q K^T in shared memory (TMEM is full: S and O of two streams) a step
 // of 16 columns takes 90 cycles instead of 64 for reading them, and each half of a tile
@@ -279,7 +279,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) {      // n lowest bits
 // Joins the parts of one row in the order of their keys, 4 kC columns at a time with the
 // loads of kP parts in flight.  A warp's rows lie side by side.  This is at the end of
 // most CTAs' work, and its time is that of the loads one after another: with 16 columns
-// of one part in flight it took 15 us, so that six ragged chunks took 120 us for 108.
+// of one part in flight it took 15 us, so that five ragged chunks took 120 us for 108.
 template <int D, int kC, int kP>
 __device__ __forceinline__ void join_row(const float* slots, size_t slot_n, int nparts, int row,
                                          __nv_bfloat16* out, bool out32, float* lse) {
@@ -1085,15 +1085,15 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // Where a run of 16 rows or more divides both page and tile, tiles are full whatever
   // the page.  Otherwise a tile has whole pages, or a page whole tiles, and masked
   // columns.  Runs of 8 rows fill them too, but their many copies cost as much as
-  // tiles of which a quarter is empty: they are taken where less than 7/8 would be
-  // filled.  (Eight chunks of 256 tokens over 8,000 keys, 32 on 8 heads of 128: full
-  // tiles by runs of 16 and more 272 us, of 8 rows 363 us; masked tiles 322 us for
-  // pages of 1,000 rows, 330 us for 40, 386 us for 200, 392 us for 48.)
+  // tiles of 100 keys: they are taken where fewer would be in one.  (Eight chunks of
+  // 256 tokens over 8,000 keys, 32 on 8 heads of 128: full tiles by runs of 16 and more
+  // 260 us, of 8 rows 346 us; masked tiles of 125 keys 286 us, 120 298, 112 310, 104
+  // 330, 100 346, 72 468.)
   int fit = kTile;
   while (a.B % fit != 0) fit /= 2;
   const int padded = (a.B + 7) / 8 * 8, tiles_page = (a.B + kTile - 1) / kTile;
   const int filled = a.B < kTile ? kTile / padded * a.B : a.B / tiles_page;   // keys of a tile
-  const bool full = fit >= 16 || (fit == 8 && filled < kTile * 7 / 8);
+  const bool full = fit >= 16 || (fit == 8 && filled < 100);
   const bool small = !full && a.B < kTile;
   p.run_rows = full ? fit : small ? padded : kTile;
   p.run_tokens = small ? a.B : p.run_rows;

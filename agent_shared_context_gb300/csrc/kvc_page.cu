@@ -255,7 +255,7 @@ constexpr int kWriteVecs = 4;                    // vectors per thread, all in f
 // or slot numbers beyond 31 bits (64-bit divisions made the copy wait for
 // arithmetic: two trajectories of 10,240 tokens took 1,051 us with them; they take
 // 746 us now, 5.37 GB at 7.2 TB/s, 1.06 of a device copy's rate).  A step's rows of
-// one layer, 16 tokens or 2,048, take 8 to 9 us, most of it the host's.
+// one layer, 16 tokens or 2,048, take 7 to 8.5 us, most of it the host's.
 template <bool BIG>
 __global__ void __launch_bounds__(kWriteThreads)
     page_write_kernel(const WriteArgs a, const FastDiv per_src, const FastDiv per_page,
