@@ -193,7 +193,8 @@ struct Shares {
   }
   __device__ __forceinline__ int owner(int64_t u) const {
     const int64_t x = (u + 1) * n - 1;
-    if (x < (int64_t(1) << 32)) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(U));
+    if ((x | U) < (int64_t(1) << 32))
+      return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(U));
     return static_cast<int>(x / U);
   }
 };

@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes);
         __syncwarp();
         if (lane < boxes)
-          tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64, use.row,
-                      it.h, a.layer, use.page);
+          tma_load_5d(my_dst + s * C::kSlotBytes, is_v ? &maps.v : &maps.k, bar, my_sub * 64,
+                      use.row, it.h, a.layer, use.page);
         ++ring;
         if (++s == NS) {
           s = 0;

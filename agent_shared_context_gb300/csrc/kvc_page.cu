@@ -330,7 +330,8 @@ cudaError_t launch_page_write(const WriteArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.rows + rows_cta - 1) / rows_cta),
                   static_cast<unsigned>(a.nl * a.H), 2);
   const int64_t most = int64_t(1) << 31;
-  auto* fn = a.rows >= most || a.n_slots >= most ? page_write_kernel<true> : page_write_kernel<false>;
+  auto* fn =
+      a.rows >= most || a.n_slots >= most ? page_write_kernel<true> : page_write_kernel<false>;
   return launch_early(fn, grid, kWriteThreads, 0, stream, a, attn::make_fastdiv(a.T),
                       attn::make_fastdiv(a.B), attn::make_fastdiv(a.vec_row));
 }
