@@ -107,3 +107,42 @@ def test_served_chain_refusals():
         paged.PagedCache(1, 2, 96, "bf16", 8, 4, 16, 2, 3, 32)   # bf16 heads are 64 or 128
     pc.plan([40, 8], 32)
     assert pc.plan_status.tolist()[0] != 0 and pc.kv_lens.tolist()[0] == 4
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_steps_that_follow_one_another(dtype, d):
+    """Plan, write and attention of many small steps without a pause between them (each
+    kernel is launched while the one before ends) give the bits of steps that wait."""
+    from agent_shared_context_gb300 import paged
+    R, H, Hq, B = 5, 2, 8, 16
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    steps = [[1] * R if i % 3 else [(7 * i + 3 * r) % 40 for r in range(R)] for i in range(30)]
+    lens = [torch.tensor(s, dtype=torch.int32, device="cuda") for s in steps]
+    rows = [[torch.randn((sum(s), h, d), generator=g, device="cuda").to(dt) for h in (Hq, H, H)]
+            for s in steps]
+    blocks = sum(max(s) for s in steps) // B + 1
+
+    def run(wait):
+        pc = paged.PagedCache(1, H, d, dtype, Hq, R * blocks, B, R, blocks, 40 * R)
+        outs = []
+        torch.cuda.synchronize()
+        for s, n, (q, k, v) in zip(steps, lens, rows):
+            pc.plan(n, sum(s))
+            if wait:
+                torch.cuda.synchronize()
+            pc.write(0, k, v)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(pc.attend(0, q))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert not pc.plan_status.any() and not int(pc.dev_status)
+        return outs, pc.kv_lens.tolist()
+
+    want, kv = run(True)
+    assert kv == [sum(s[r] for s in steps) for r in range(R)]
+    for _ in range(5):
+        got, _ = run(False)
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
