@@ -518,8 +518,8 @@ typedef struct kvc_attn_params {
  * rounded to bf16 for the product with V and the remainder of those that carry
  * much of their row multiplied too; up to 128 rows of no more tokens than
  * requests run in a decoding kernel on warp-level tensor-core instructions.
- * f32 runs on these with every factor split into two tf32 numbers: 21 bits or
- * more of each product are kept (11 for factors below 2^-115).
+ * f32 runs on these with every factor split into two tf32 numbers: a product
+ * is off by at most 5 2^-22 of itself (by 2^-10 for factors below 2^-115).
  *
  * `workspace` holds kvc_paged_attention_workspace() bytes (0 for descriptors
  * that the call would refuse), 256-byte aligned.  ITS FIRST 8,192 BYTES MUST
