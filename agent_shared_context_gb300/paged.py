@@ -153,7 +153,8 @@ def from_chain(runner: ChainRunner, agent: int, n_q_heads: int, new_tokens: int,
 def decode_graph(pc: PagedCache, new_lens: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                  v: torch.Tensor, out: torch.Tensor) -> torch.cuda.CUDAGraph:
     """Two steps over all layers as a CUDA graph: tokens ``q``, ``out``
-    [2, L, N, n_q_heads, d] and ``k``, ``v`` [2, L, N, H, d], read at replay."""
+    [2, L, N, n_q_heads, d] and ``k``, ``v`` [2, L, N, H, d], read at replay.
+    The graph keeps them, ``new_lens`` and the cache for as long as it lives."""
     if pc.stream is not None:
         raise ValueError("a captured step runs on the capturing stream: stream=None")
 
@@ -168,6 +169,7 @@ def decode_graph(pc: PagedCache, new_lens: torch.Tensor, q: torch.Tensor, k: tor
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         two_steps(new_lens)
+    graph.buffers = (pc, new_lens, q, k, v, out)         # which a replay reads and writes
     return graph
 
 
