@@ -18,7 +18,8 @@ other one, the held cache of agent j - 1): a chain then needs the exact caches
 of its agents, every edge's anchor inputs and two cache-sized outputs, instead
 of one output per edge.  Only the PH rows of a reused buffer are rewritten;
 its PF rows keep the agent-specific prefix of the agent it was created for,
-which no call of the chain reads.
+which no call of the chain reads.  Who reads whole caches asks ``holds`` (edge
+j + 2 writes over agent j's rows) and ``own_prefix``.
 
 All arithmetic of the correction path runs in libkvc; this module only
 allocates device memory with torch and passes pointers.
@@ -83,8 +84,9 @@ class ChainRunner:
         self.workspace = torch.empty(max(ws, 256) // 4, dtype=torch.float32, device=dev)
         bws = kvc.kvc_build_states_workspace(self.seg, self.prm) if self.build else 0
         self.build_ws = torch.empty(max(bws, 256), dtype=torch.uint8, device=dev)
-        mask = ph_row_mask(wl, dev)
+        self.ph_rows = mask = ph_row_mask(wl, dev)
         self.keep_outputs = keep_outputs
+        self._buffer_of = [1, 2]      # whose cache each of the alternating buffers holds
         self.edges: List[Optional[EdgeOutputs]] = [None]
         for j in range(1, wl.edges + 1):
             if not keep_outputs and j > 2:
@@ -119,6 +121,15 @@ class ChainRunner:
             return self.inp.exact_K[0], self.inp.exact_V[0]
         return self.edges[j].out_K, self.edges[j].out_V
 
+    def holds(self, j: int) -> bool:
+        """Whether the buffers of ``held(j)`` hold agent j's cache: alternating
+        ones do from edge j until edge j + 2."""
+        return self.keep_outputs or j == 0 or self._buffer_of[(j - 1) % 2] == j
+
+    def own_prefix(self, j: int) -> bool:
+        """Whether the PF rows of ``held(j)`` are agent j's."""
+        return self.keep_outputs or j <= 2
+
     def run_edge(self, j: int) -> None:
         wl, inp = self.wl, self.inp
         refK, refV = self.held(j - 1) if self.fixed_ref is None else self.fixed_ref
@@ -141,6 +152,8 @@ class ChainRunner:
                            e.W_V, dK, dV, eo.out_K, eo.out_V, eo.weights, eo.best, eo.score,
                            eo.fallback, self.workspace, self.dev_status, stream=self.stream,
                            ksum_in=ksum_in, ksum_out=eo.ksum)
+        if not self.keep_outputs:
+            self._buffer_of[(j - 1) % 2] = j
 
     def run(self) -> None:
         for j in range(1, self.wl.edges + 1):

@@ -105,15 +105,20 @@ class PagedCache:
         kvc.kvc_page_write(self.pg, view(K), view(V), self.slots, self.pool_K, self.pool_V, layer,
                            stream=self.stream)
 
-    def load(self, K: torch.Tensor, V: torch.Tensor) -> None:
+    def load(self, K: torch.Tensor, V: torch.Tensor, rows: Optional[torch.Tensor] = None) -> None:
         """All layers of dense caches [requests, L, H, T, d] into the pages of
-        the tokens just planned (T of each request)."""
+        the tokens just planned (T of each request); of those, where ``rows``
+        ([requests, T] bool) is given, only the ones that it names."""
         if K.dim() != 5 or V.shape != K.shape or K.shape[:3] != (self.pg.R, self.pg.L, self.pg.H):
             raise ValueError("dense caches are [requests, L, H, T, d]")
         if K.shape[0] * K.shape[3] > self._planned:
             raise ValueError("more tokens than were planned")
-        kvc.kvc_page_write(self.pg, K, V, self.slots, self.pool_K, self.pool_V, 0,
-                           stream=self.stream)
+        with torch.cuda.stream(self.stream):
+            slots = self.slots
+            if rows is not None:
+                slots = torch.where(rows.reshape(-1), slots[:rows.numel()], -1)
+            kvc.kvc_page_write(self.pg, K, V, slots, self.pool_K, self.pool_V, 0,
+                               stream=self.stream)
 
     def attend(self, layer: int, q: torch.Tensor, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, causal: bool = True, window: int = 0,
@@ -139,7 +144,11 @@ class PagedCache:
 def from_chain(runner: ChainRunner, agent: int, n_q_heads: int, new_tokens: int,
                page_size: int = 16) -> PagedCache:
     """Pages that hold agent ``agent``'s held caches of every request, with
-    room for ``new_tokens`` more per request."""
+    room for ``new_tokens`` more per request.  A chain that reuses its output
+    buffers hands out the agents whose rows are still there."""
+    if not runner.holds(agent):
+        raise ValueError("agent %d's cache is not in its buffer: the chain reuses them "
+                         "(keep_outputs=False)" % agent)
     K, V = runner.held(agent)
     R, L, H, T, d = K.shape
     blocks = -(-(T + new_tokens) // page_size)
@@ -147,6 +156,8 @@ def from_chain(runner: ChainRunner, agent: int, n_q_heads: int, new_tokens: int,
                     R * max(T, new_tokens), device=K.device, stream=runner.stream)
     pc.plan([T] * R, R * T)
     pc.load(K, V)
+    if not runner.own_prefix(agent):
+        pc.load(runner.inp.exact_K[agent], runner.inp.exact_V[agent], ~runner.ph_rows)
     return pc
 
 

@@ -30,3 +30,50 @@ def test_captured_steps_keep_their_tensors():
         torch.cuda.synchronize()
         assert pc.kv_lens.tolist() == [step] * 3 and not pc.plan_status.any()
     assert all((x == 77).all() for x in junk)
+
+
+def _rows(pc, K, r, T):
+    """[L, H, T, d]: the first T rows of request r out of the pool ``K``."""
+    B = pc.pg.page_size
+    pages = K[pc.table[r, :-(-T // B)].long()]                    # [n, L, H, B, d]
+    return pages.permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :T]
+
+
+def _runners(**kw):
+    from agent_shared_context_gb300 import synth
+    from agent_shared_context_gb300.chain import ChainRunner
+    wl = synth.scaled(synth.workload("llama2k"), L=2, H=2, R=2, seg_len=[64, 72], pf=24, **kw)
+    inp = synth.generate(wl, device="cuda")
+    return wl, ChainRunner(wl, inp), ChainRunner(wl, inp, keep_outputs=False)
+
+
+def test_context_of_a_memory_lean_chain():
+    """A chain that alternates between two buffers hands out the same context as one that
+    keeps them all: an agent's own tokens are its own."""
+    from agent_shared_context_gb300 import paged
+    wl, full, lean = _runners()
+    assert wl.edges == 3
+    full.run(), lean.run()
+    for agent in (0, 2, 3):
+        a, b = (paged.from_chain(x, agent, 8, 5, 16) for x in (full, lean))
+        for r in range(wl.R):
+            for x, y, held in zip((a.pool_K, a.pool_V), (b.pool_K, b.pool_V), full.held(agent)):
+                assert torch.equal(_rows(a, x, r, wl.T), held[r])
+                assert torch.equal(_rows(b, y, r, wl.T), held[r]), agent
+    with pytest.raises(ValueError):
+        paged.from_chain(lean, 1, 8, 5, 16)                       # agent 3's rows are there
+
+
+def test_context_of_a_memory_lean_chain_between_its_edges():
+    from agent_shared_context_gb300 import paged
+    wl, full, lean = _runners()
+    for j in range(1, wl.edges + 1):
+        full.run_edge(j), lean.run_edge(j)
+        b = paged.from_chain(lean, j, 8, 5, 16)
+        for r in range(wl.R):
+            for x, held in zip((b.pool_K, b.pool_V), full.held(j)):
+                assert torch.equal(_rows(b, x, r, wl.T), held[r]), j
+        for other in range(j + 1, wl.edges + 1):
+            if other > 2:
+                with pytest.raises(ValueError):
+                    paged.from_chain(lean, other, 8, 5, 16)       # its edge has not run
