@@ -12,8 +12,8 @@
 // and output of its keys.  The four warps' results are joined at the end of an
 // item.
 //
-// The mathematics is that of kvc_attn_f32.cu, P enters the product with V as
-// bf16(P) and the remainder P - bf16(P): the tensor core has time for both.
+// The mathematics is that of kvc_attn_f32.cu, P enters the product with V as two
+// numbers (cut_bf16 and the rest of it): the tensor core has time for both.
 //
 // Rows of keys beyond the request's, or out of all rows' sight, are filled with
 // zeros instead of being read, so what a page holds there cannot reach a sum.
@@ -306,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
           for (int n = 0; n < kG; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float p0 = s[g8][n][2 * h], p1 = s[g8][n][2 * h + 1];
-              const uint32_t u = pack_bf16(p0, p1);
+              const uint64_t p2 = ptx::pack_f32x2(__float_as_uint(s[g8][n][2 * h]),
+                                                  __float_as_uint(s[g8][n][2 * h + 1]));
+              const uint32_t u = ptx::cut_bf16(p2);
               ph[g8][n][h] = transpose8x8(u);
-              pl[g8][n][h] = transpose8x8(
-                  pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u)));
+              pl[g8][n][h] = transpose8x8(ptx::rest_bf16(p2, u));
             }
           if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll

@@ -42,10 +42,10 @@
 //
 // The product with V takes P as bf16 (its sum l stays fp32).  Roundings of up to
 // 2^-8 average out over many keys of like weight but not where few carry a
-// row, so the remainder P - bf16(P) is multiplied too, in the steps of 16 keys
-// in which some row has a key with more than 1/8 of its sum so far (1/16 in
-// single mode, which waits for memory anyway): few steps of a long context.  S
-// leaves room for it in TMEM, beside P.
+// row, so in the steps of 16 keys in which some row has a key with more than 1/8
+// of its sum so far (1/16 in single mode, which waits for memory anyway) P enters
+// as two numbers, cut_bf16 and the rest of it: few steps of a long context.  S
+// leaves room for the rest in TMEM, beside P.
 //
 // Measured: dense prefill of two contexts of 8,192 tokens, 32 query heads on 8 of 128,
 // 0.97 ms, 1.14 PFLOP/s or 0.60 of the library's matrix products; sixteen chunks of 128
@@ -124,7 +124,7 @@ struct ItemSlot {
 
 // What a stream's softmax tells its MMA warp along with P.
 struct alignas(8) Told {
-  uint32_t heavy;          // MMA steps of 16 keys with a remainder, a byte per warp
+  uint32_t heavy;          // MMA steps of 16 keys with P as two numbers, a byte per warp
   int32_t o_init;          // O holds something before the first P V
 };
 
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             static_assert(kHalf == 64, "four steps of 16 keys");
             mma_bf16_ts_x4(dO, tS_h, dvh, kIdescO, acc);
             if (heavy != 0) {
-              // the remainders of P, for the warps that have one in the step
+              // the rest of P, for the warps that have one in the step
 #pragma unroll 1
               for (int k = 0; k < kHalf / 16; ++k) {
                 const uint32_t who = (heavy >> k) & 0x01010101u;
@@ -843,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                              valid && exp2_fast(fmaf(mx[g], a.scale_log2, -ref)) > least))
                 heavy |= 1u << g;
           }
-          // P, and its remainder where it is wanted, in passes without branches, so that
-          // the exponentials of many keys are in flight
+          // P, in passes without branches, so that the exponentials of many keys are in
+          // flight: 64 where no step needs two numbers, 16 elsewhere
           uint64_t sum[2] = {0, 0};
           auto two = [&](int j) {                            // keys j, j + 1
             float p0, p1;
@@ -860,17 +860,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kHalf; j += 2) two(j);
           } else {
-            const uint64_t minus1 = pack_f32x2(0xbf800000u, 0xbf800000u);
-            uint32_t rest[kHalf / 2];
 #pragma unroll
-            for (int j = 0; j < kHalf; j += 2) {
-              const uint64_t p2 = two(j);
-              const uint32_t u = x[j >> 1];
-              float r0, r1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(u << 16, u & 0xffff0000u), minus1, p2), r0, r1);
-              rest[j >> 1] = pack_bf16(r0, r1);
+            for (int g = 0; g < 4; ++g) {
+              if (((heavy >> g) & 1u) == 0) {
+#pragma unroll
+                for (int j = 16 * g; j < 16 * g + 16; j += 2) two(j);
+                continue;
+              }
+              uint32_t rest[8];
+#pragma unroll
+              for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                const uint64_t p2 = two(j);
+                x[j >> 1] = cut_bf16(p2);
+                rest[(j >> 1) & 7] = rest_bf16(p2, x[j >> 1]);
+              }
+              tmem_st_32x32b_x8(sH + kHalf / 2 + 8 * g, rest);
             }
-            tmem_st_32x32b_x32(sH + kHalf / 2, rest);
           }
           tmem_st_32x32b_x32(sH, x);
           {
@@ -897,9 +902,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const TileSpan t = tile_span(p, it.tile0 + i);
               const int tok = tile_tok(p, t, n + half * kHalf), blk = fast_div(tok, p.page);
               const int page = a.table[static_cast<int64_t>(it.r) * a.width + blk];
+              auto half_of = [&](uint32_t two_p) {
+                return __uint_as_float((n & 1) ? two_p & 0xffff0000u : two_p << 16);
+              };
               const uint32_t two_p = tmem_ld_32x32b_x1(sH + (n >> 1));
+              const uint32_t two_r = tmem_ld_32x32b_x1(sH + kHalf / 2 + (n >> 1));
               tmem_ld_wait();
-              const float pr = __uint_as_float((n & 1) ? two_p & 0xffff0000u : two_p << 16);
+              const float pr =
+                  half_of(two_p) + ((heavy >> (n >> 4)) & 1u ? half_of(two_r) : 0.f);
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool[1].base) +
                                        page * a.pool[1].s_req + a.layer * a.pool[1].s_layer +
                                        it.h * a.pool[1].s_head +

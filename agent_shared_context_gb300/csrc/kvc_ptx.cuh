@@ -309,6 +309,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -350,6 +357,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// ------------------------------------------- probabilities as two bf16 numbers
+// P = cut + rest, P >= 0: cut has P's upper 16 bits, rest what is missing and 2^-20
+// of cut more, so that it is 0 only where P is.  Then cut v + rest v is right for an
+// infinite v as well (with P rounded, rest may have the other sign, and 0 where P is
+// exact gives NaN).  rest is below 2^-7 P and off by 2^-9 of itself as bf16: cut +
+// rest is P to 2^-16 + 2^-20.  Two at a time, the first in the lower half.
+__device__ __forceinline__ uint32_t cut_bf16(uint64_t p2) {
+  float p0, p1;
+  unpack_f32x2(p2, p0, p1);
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+}
+__device__ __forceinline__ uint32_t rest_bf16(uint64_t p2, uint32_t cut) {
+  const uint64_t less = pack_f32x2(0xbf7ffff0u, 0xbf7ffff0u);     // -(1 - 2^-20)
+  float r0, r1;
+  unpack_f32x2(fma_f32x2(pack_f32x2(cut << 16, cut & 0xffff0000u), less, p2), r0, r1);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(r1), "f"(r0));
+  return r;
 }
 
 // Shared-memory matrix descriptor (tcgen05), K-major operand in the 128-byte

@@ -513,11 +513,14 @@ typedef struct kvc_attn_params {
  * A row that sees no key gets out = 0 and lse = -inf.  Key and value rows at
  * or beyond kv_lens[r] are never used, whatever they hold.  n == 1 is
  * decoding; requests with one token, with many and with none may be mixed.
+ * An infinite value gives the rows that see it an infinity of its sign, NaN beside
+ * one of the other sign; where its weight is below 2^-90 of the row's largest it may
+ * be left out or give NaN.
  * Rows of no request are not written.  All sums, maxima and the softmax
  * are fp32.  bf16: chunks run on tcgen05 tensor cores, with the probabilities
- * rounded to bf16 for the product with V and the remainder of those that carry
- * much of their row multiplied too; up to 128 rows of no more tokens than
- * requests run in a decoding kernel on warp-level tensor-core instructions.
+ * rounded to bf16 for the product with V, or as two bf16 numbers (16 bits) where a
+ * key carries much of its row; up to 128 rows of no more tokens than requests run
+ * in a decoding kernel on warp-level tensor-core instructions, with two numbers.
  * f32 runs on these with every factor split into two tf32 numbers: a product
  * is off by at most 5 2^-22 of itself (by 2^-10 for factors below 2^-115).
  *

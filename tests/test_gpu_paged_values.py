@@ -1,0 +1,88 @@
+"""Paged attention where the values, the mask or the table are at a limit of what a
+call takes, against the float64 oracle (tolerances: test_gpu_paged).
+
+A value row with an infinity gives every row that sees it the infinity of the formula,
+sum_j p_j v_j with p_j > 0: its sign in that column, NaN where infinities of both signs
+are seen.  The scores here are within 30 of one another, so that no p_j underflows."""
+import numpy as np
+import pytest
+import torch
+
+from .test_gpu_paged import FEW, Batch
+
+pytestmark = pytest.mark.gpu
+
+CHUNKS = [(40, 200), (1, 77), (130, 131), (3, 3), (1, 1), (0, 9)]
+
+
+def _key(b, r, j):
+    """(page, row) of key j of request r."""
+    return b.table[r, j // b.B], j % b.B
+
+
+def _sees(b, r, j, causal, window):
+    """[N] bool: the rows that see key j of request r."""
+    seen = np.zeros(b.N, dtype=bool)
+    n, kv = b.lens[r]
+    for i in range(n):
+        p = kv - n + i
+        seen[b.q_start[r] + i] = (not causal or j <= p) and (not window or j > p - window)
+    return seen
+
+
+@pytest.mark.parametrize("lens", [FEW, CHUNKS], ids=["few", "chunks"])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("G", [1, 2, 12])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 30)])
+def test_infinite_values_in_sight(lens, dtype, d, G, causal, window):
+    b = Batch(lens, 2 * G, 2, d, 20, dtype, seed=G)
+    want = np.zeros((b.N, 2 * G, d))               # infinities of each sign that a row sees
+    minus = np.zeros_like(want)
+    for r, (_, kv) in enumerate(b.lens):
+        for j, head, col, sign in [(0, 0, 0, 1), (kv // 2, 0, 3, -1), (kv - 1, 0, d - 1, 1),
+                                   (kv // 3, 1, 7, 1), (2 * kv // 3, 1, 7, -1),
+                                   (kv - 1, 1, 8, -1)]:
+            if not 0 <= j < kv:
+                continue
+            page, row = _key(b, r, j)
+            b.host[1][page, 0, head, row, col] = 0.0
+            if not b.V[page, 0, head, row, col].isinf():
+                b.V[page, 0, head, row, col] = sign * float("inf")
+                seen = _sees(b, r, j, causal, window)
+                to = want if sign > 0 else minus
+                to[seen, head * G:head * G + G, col] = 1
+    plus, minus = torch.from_numpy(want).cuda() > 0, torch.from_numpy(minus).cuda() > 0
+    b.run(causal, window)
+    got = b.out.clone()
+    assert got[plus & minus].isnan().all()
+    assert (got[plus & ~minus] == float("inf")).all()
+    assert (got[minus & ~plus] == float("-inf")).all()
+    b.V.copy_(b.host[1])
+    b.run(causal, window)
+    b.out.copy_(torch.where(plus | minus, b.out, got))   # the rest is what it is without them
+    b.check(causal, window)
+
+
+@pytest.mark.parametrize("lens", [FEW, CHUNKS], ids=["few", "chunks"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_odd_keys_in_sight(lens, d, value):
+    """A score of -inf has no weight, one of +inf or NaN no softmax."""
+    G = 2
+    b = Batch(lens, 2 * G, 2, d, 20, "bf16", seed=5)
+    r, j = 1, 0
+    page, row = _key(b, r, j)
+    b.K[page, 0, 0, row, 2] = value
+    b.run()
+    got = b.out.clone()
+    rows = torch.from_numpy(_sees(b, r, j, True, 0)).cuda()
+    up = b.q[:, :G, 2].float() * value
+    bad = torch.zeros(b.N, 2 * G, dtype=torch.bool, device="cuda")
+    bad[:, :G] = rows[:, None] & ~(up == float("-inf"))
+    assert got[bad].isnan().all() and got[~bad].isfinite().all()
+    other = ~rows[:, None].expand(-1, 2 * G).clone()     # what does not see it
+    other[:, G:] = True
+    b.K.copy_(b.host[0])
+    b.run()
+    b.out.copy_(torch.where(other[:, :, None], got, b.out))
+    b.check()
