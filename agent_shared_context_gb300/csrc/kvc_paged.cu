@@ -350,7 +350,9 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
   a.width = pg->max_blocks;
   a.layer = at->layer;
   a.causal = at->causal;
-  a.window = at->window;
+  // positions stay below 2^30: a window as long as that hides nothing, and the kernels'
+  // sums of a position (down to -2^30) and a window stay within 32 bits
+  a.window = at->window >= (1 << 30) ? 0 : at->window;
   a.scale_log2 = at->scale * 1.4426950408889634f;
   a.workspace = workspace;
   a.dev_status = dev_status;

@@ -86,3 +86,16 @@ def test_odd_keys_in_sight(lens, d, value):
     b.run()
     b.out.copy_(torch.where(other[:, :, None], got, b.out))
     b.check()
+
+
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 64, 1), ("bf16", 128, 1), ("bf16", 128, 4),
+                                       ("bf16", 64, 12), ("f32", 64, 1), ("f32", 80, 4)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 300, 2 ** 30, 2 ** 30 - 1])
+@pytest.mark.parametrize("lens", [[(9, 4), (6, 2), (1, 700)] + [(0, 3)] * 20,
+                                  [(9, 4), (300, 10), (700, 200), (1, 700), (40, 400)]],
+                         ids=["few", "chunks"])
+def test_windows_longer_than_any_context(dtype, d, G, window, lens):
+    """Also with more new tokens than keys, whose first positions are negative."""
+    b = Batch(lens, 2 * G, 2, d, 16, dtype, seed=G)
+    b.run(True, window)
+    b.check(True, window)
