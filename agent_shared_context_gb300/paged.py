@@ -99,8 +99,9 @@ class PagedCache:
     def write(self, layer: int, K: torch.Tensor, V: torch.Tensor) -> None:
         """The planned tokens' rows [N, H, d] into their pages of a layer."""
         self._tokens(K)
-        if V.shape != K.shape:
-            raise ValueError("K and V are [N, H, d]")
+        self._tokens(V)
+        if K.shape[1] != self.pg.H or V.shape != K.shape:
+            raise ValueError("K and V are [N, H, d] with the pools' heads")
         view = lambda x: x.permute(1, 0, 2)[None, None]  # noqa: E731   [1, 1, H, N, d]
         kvc.kvc_page_write(self.pg, view(K), view(V), self.slots, self.pool_K, self.pool_V, layer,
                            stream=self.stream)
@@ -137,8 +138,11 @@ class PagedCache:
     def _tokens(self, x: torch.Tensor) -> None:
         if x.dim() != 3 or x.shape[0] > self._planned or x.shape[2] != self.pg.d:
             raise ValueError("a step's rows are [N, heads, d], no more than were planned")
-        if x.dtype != self.pool_K.dtype:
-            raise ValueError("a step's rows have the pools' type")
+        self._like_pools(x)
+
+    def _like_pools(self, x: torch.Tensor) -> None:
+        if x.dtype != self.pool_K.dtype or x.device != self.pool_K.device:
+            raise ValueError("what goes with the pools has their type and is on their device")
 
 
 def from_chain(runner: ChainRunner, agent: int, n_q_heads: int, new_tokens: int,

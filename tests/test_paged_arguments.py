@@ -1,0 +1,44 @@
+"""PagedCache refuses tensors that do not fit its pools before anything is launched.
+The tensors lie in host memory, so that no launch could take them: no GPU is needed."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from agent_shared_context_gb300 import paged  # noqa: E402
+
+OTHER = {"bf16": torch.float32, "f32": torch.bfloat16}
+
+
+def _cache(dtype, planned=6, device="cpu"):
+    """2 layers, 4 KV heads of 64, 8 query heads, 2 requests; `planned` tokens."""
+    pc = paged.PagedCache(2, 4, 64, dtype, 8, 16, 8, 2, 4, 12, device=device)
+    pc._planned = planned
+    return pc
+
+
+@pytest.fixture(params=["bf16", "f32"])
+def pc(request):
+    return _cache(request.param)
+
+
+def _other(pc):
+    return torch.float32 if pc.pool_K.dtype == torch.bfloat16 else torch.bfloat16
+
+
+def _refused(call, *args, **kw):
+    with pytest.raises(ValueError) as e:
+        call(*args, **kw)
+    return str(e.value)
+
+
+def test_write_refuses_rows_that_do_not_fit(pc):
+    dt = pc.pool_K.dtype
+    good = torch.zeros((6, 4, 64), dtype=dt)
+    for heads in (1, 3, 5, 8):                     # fewer would be read past their end
+        bad = torch.zeros((6, heads, 64), dtype=dt)
+        assert "heads" in _refused(pc.write, 0, bad, bad)
+    for bad in (good.to(_other(pc)), good[:5], good[:, :3], good[:, :, :32],
+                torch.zeros((6, 4, 64), dtype=dt, device="meta")):
+        _refused(pc.write, 0, good, bad)
+        _refused(pc.write, 0, bad, good)
+    _refused(pc.write, 0, torch.zeros((7, 4, 64), dtype=dt), torch.zeros((7, 4, 64), dtype=dt))
