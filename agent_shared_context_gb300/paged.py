@@ -110,8 +110,14 @@ class PagedCache:
         """All layers of dense caches [requests, L, H, T, d] into the pages of
         the tokens just planned (T of each request); of those, where ``rows``
         ([requests, T] bool) is given, only the ones that it names."""
-        if K.dim() != 5 or V.shape != K.shape or K.shape[:3] != (self.pg.R, self.pg.L, self.pg.H):
+        if (K.dim() != 5 or V.shape != K.shape or K.shape[4] != self.pg.d
+                or K.shape[:3] != (self.pg.R, self.pg.L, self.pg.H)):
             raise ValueError("dense caches are [requests, L, H, T, d]")
+        self._like_pools(K)
+        self._like_pools(V)
+        if rows is not None and (rows.shape != (K.shape[0], K.shape[3]) or rows.dtype != torch.bool
+                                 or rows.device != K.device):
+            raise ValueError("rows is [requests, T] bool")
         if K.shape[0] * K.shape[3] > self._planned:
             raise ValueError("more tokens than were planned")
         with torch.cuda.stream(self.stream):

@@ -42,3 +42,19 @@ def test_write_refuses_rows_that_do_not_fit(pc):
         _refused(pc.write, 0, good, bad)
         _refused(pc.write, 0, bad, good)
     _refused(pc.write, 0, torch.zeros((7, 4, 64), dtype=dt), torch.zeros((7, 4, 64), dtype=dt))
+
+
+def test_load_refuses_caches_that_do_not_fit(pc):
+    dt = pc.pool_K.dtype
+    good = torch.zeros((2, 2, 4, 3, 64), dtype=dt)
+    for bad in (good.to(_other(pc)), good[..., :32], good[:, :, :3], good[:, :1], good[:1],
+                torch.zeros((2, 2, 4, 3, 128), dtype=dt), good[:, :, :, :2],
+                torch.zeros((2, 2, 4, 3, 64), dtype=dt, device="meta")):
+        _refused(pc.load, good, bad)
+        _refused(pc.load, bad, good)
+    for bad in (good.to(_other(pc)), good[..., :32],
+                torch.zeros((2, 2, 4, 4, 64), dtype=dt)):           # more than was planned
+        _refused(pc.load, bad, bad)
+    for rows in (torch.ones((2, 4), dtype=torch.bool), torch.ones((2, 3)),
+                 torch.ones(6, dtype=torch.bool), torch.ones((2, 3), dtype=torch.bool, device="meta")):
+        _refused(pc.load, good, good, rows)
