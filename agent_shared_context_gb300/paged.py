@@ -87,8 +87,9 @@ class PagedCache:
             raise ValueError("a step brings at most max_tokens tokens")
         if not isinstance(new_lens, torch.Tensor):
             new_lens = torch.tensor(new_lens, dtype=torch.int32, device=self.device)
-        if new_lens.dtype != torch.int32 or new_lens.shape != (self.pg.R,):
-            raise ValueError("new_lens is [requests] int32")
+        if (new_lens.dtype != torch.int32 or new_lens.shape != (self.pg.R,)
+                or new_lens.device != self.table.device):
+            raise ValueError("new_lens is [requests] int32, on the pools' device")
         old, new = self._now, 1 - self._now
         kvc.kvc_page_plan(self.pg, new_lens.contiguous(), self._kv_lens[old], self._kv_lens[new],
                           self.table, self.free_pages, self._n_free[old], self._n_free[new],
@@ -130,11 +131,16 @@ class PagedCache:
     def attend(self, layer: int, q: torch.Tensor, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, causal: bool = True, window: int = 0,
                scale: float = 0.0) -> torch.Tensor:
-        """Attention of the planned tokens' queries [N, n_q_heads, d]."""
+        """Attention of the planned tokens' queries [N, n_q_heads, d]; ``lse``
+        [N, n_q_heads] float32 gets the logarithms of the softmax's sums."""
         self._tokens(q)
         if q.shape[1] > self.n_q_heads:
             raise ValueError("more query heads than n_q_heads")
         out = torch.empty_like(q) if out is None else out
+        self._like_pools(out)
+        if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
+                                or lse.device != q.device or not lse.is_contiguous()):
+            raise ValueError("lse is [N, n_q_heads] float32, contiguous")
         at = kvc.attn_params(q, out, layer, scale, causal, window)
         kvc.kvc_paged_attention(self.pg, at, q, self.pool_K, self.pool_V, self.table, self.q_start,
                                 self.kv_lens, out, self.workspace, self.dev_status, lse=lse,

@@ -58,3 +58,24 @@ def test_load_refuses_caches_that_do_not_fit(pc):
     for rows in (torch.ones((2, 4), dtype=torch.bool), torch.ones((2, 3)),
                  torch.ones(6, dtype=torch.bool), torch.ones((2, 3), dtype=torch.bool, device="meta")):
         _refused(pc.load, good, good, rows)
+
+
+def test_attend_refuses_outputs_that_do_not_fit(pc):
+    dt = pc.pool_K.dtype
+    q = torch.zeros((6, 8, 64), dtype=dt)
+    for bad in (q.to(_other(pc)), q[:5], q[:, :4], torch.zeros((6, 8, 128), dtype=dt),
+                torch.zeros((6, 8, 64), dtype=dt, device="meta"),
+                torch.zeros((6, 64, 8), dtype=dt).transpose(1, 2)):
+        _refused(pc.attend, 0, q, bad)
+    for bad in (torch.zeros((6, 8), dtype=torch.float16), torch.zeros((6, 8), dtype=torch.float64),
+                torch.zeros((5, 8)), torch.zeros((6, 4)), torch.zeros(48), torch.zeros((8, 6)).T,
+                torch.zeros((6, 8), device="meta")):
+        assert "lse" in _refused(pc.attend, 0, q, lse=bad)
+    for bad in (torch.zeros((6, 8, 64), dtype=dt, device="meta"), q.to(_other(pc))):
+        _refused(pc.attend, 0, bad)
+
+
+def test_plan_refuses_lengths_elsewhere(pc):
+    for bad in (torch.zeros(2, dtype=torch.int32, device="meta"), torch.zeros(2, dtype=torch.int64),
+                torch.zeros((2, 1), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)):
+        _refused(pc.plan, bad)
