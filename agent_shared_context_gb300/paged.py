@@ -37,7 +37,11 @@ _DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 class PagedCache:
     """Pools [n_pages, L, H, page_size, d] and the state of up to ``requests``
     requests of at most ``max_blocks`` pages; a step brings at most
-    ``max_tokens`` new tokens with ``n_q_heads`` query heads."""
+    ``max_tokens`` new tokens with ``n_q_heads`` query heads.
+
+    With a ``stream`` the state above is made on it and every call runs on it,
+    behind what the current stream was given before the call; who reads state
+    or results elsewhere waits for ``stream``."""
 
     def __init__(self, L: int, H: int, d: int, dtype: str, n_q_heads: int, n_pages: int,
                  page_size: int, requests: int, max_blocks: int, max_tokens: int,
@@ -47,25 +51,28 @@ class PagedCache:
         self.n_q_heads, self.max_tokens = n_q_heads, max_tokens
         self.device, self.stream = dev, stream
         self.pg = kvc.paged(n_pages, page_size, L, H, d, dtype, requests, max_blocks)
-        self.pool_K = torch.zeros((n_pages, L, H, page_size, d), dtype=_DTYPES[dtype], device=dev)
-        self.pool_V = torch.zeros_like(self.pool_K)
-        self.table = torch.zeros((requests, max_blocks), **i32)
-        self.free_pages = torch.arange(n_pages - 1, -1, -1, **i32)   # page 0 is taken first
-        self._n_free = [torch.full((1,), n_pages, **i32), torch.zeros(1, **i32)]
-        self._kv_lens = [torch.zeros(requests, **i32) for _ in range(2)]
-        self._now = self._planned = 0
-        self.q_start = torch.zeros(requests + 1, **i32)
-        self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
-        self.positions = torch.full((max_tokens,), -1, **i32)
-        self.plan_status = torch.zeros(requests, **i32)
-        self.dev_status = torch.zeros(1, **i32)
-        # the largest step's size serves every step: it does not shrink with fewer tokens
-        q = torch.empty((max_tokens, n_q_heads, d), dtype=_DTYPES[dtype], device="meta")
-        ws = kvc.kvc_paged_attention_workspace(self.pg, kvc.attn_params(q, q))
-        if ws == 0:
-            raise ValueError("no attention of this shape: head dims are 64 or 128 in bf16, "
-                             "multiples of 4 up to 256 in f32, at most 64 query heads a KV head")
-        self.workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            self.pool_K = torch.zeros((n_pages, L, H, page_size, d), dtype=_DTYPES[dtype],
+                                      device=dev)
+            self.pool_V = torch.zeros_like(self.pool_K)
+            self.table = torch.zeros((requests, max_blocks), **i32)
+            self.free_pages = torch.arange(n_pages - 1, -1, -1, **i32)   # page 0 is taken first
+            self._n_free = [torch.full((1,), n_pages, **i32), torch.zeros(1, **i32)]
+            self._kv_lens = [torch.zeros(requests, **i32) for _ in range(2)]
+            self._now = self._planned = 0
+            self.q_start = torch.zeros(requests + 1, **i32)
+            self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
+            self.positions = torch.full((max_tokens,), -1, **i32)
+            self.plan_status = torch.zeros(requests, **i32)
+            self.dev_status = torch.zeros(1, **i32)
+            # the largest step's size serves every step: it does not shrink with fewer tokens
+            q = torch.empty((max_tokens, n_q_heads, d), dtype=_DTYPES[dtype], device="meta")
+            ws = kvc.kvc_paged_attention_workspace(self.pg, kvc.attn_params(q, q))
+            if ws == 0:
+                raise ValueError("no attention of this shape: head dims are 64 or 128 in bf16, "
+                                 "multiples of 4 up to 256 in f32, at most 64 query heads a KV "
+                                 "head")
+            self.workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
 
     @property
     def kv_lens(self) -> torch.Tensor:
@@ -86,12 +93,19 @@ class PagedCache:
         if not 0 <= tokens <= self.max_tokens:
             raise ValueError("a step brings at most max_tokens tokens")
         if not isinstance(new_lens, torch.Tensor):
-            new_lens = torch.tensor(new_lens, dtype=torch.int32, device=self.device)
+            with torch.cuda.stream(self.stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise ValueError("the lengths of a captured step are a tensor")
+                # out of pinned memory: the copy takes its turn, and nothing waits for it
+                host = torch.tensor(new_lens, dtype=torch.int32, pin_memory=True)
+                new_lens = host.to(self.device, non_blocking=True)
         if (new_lens.dtype != torch.int32 or new_lens.shape != (self.pg.R,)
                 or new_lens.device != self.table.device):
             raise ValueError("new_lens is [requests] int32, on the pools' device")
+        new_lens = new_lens.contiguous()
+        self._take(new_lens)
         old, new = self._now, 1 - self._now
-        kvc.kvc_page_plan(self.pg, new_lens.contiguous(), self._kv_lens[old], self._kv_lens[new],
+        kvc.kvc_page_plan(self.pg, new_lens, self._kv_lens[old], self._kv_lens[new],
                           self.table, self.free_pages, self._n_free[old], self._n_free[new],
                           self.q_start, self.slots, self.positions, self.plan_status,
                           stream=self.stream, max_tokens=tokens)
@@ -103,6 +117,7 @@ class PagedCache:
         self._tokens(V)
         if K.shape[1] != self.pg.H or V.shape != K.shape:
             raise ValueError("K and V are [N, H, d] with the pools' heads")
+        self._take(K, V)
         view = lambda x: x.permute(1, 0, 2)[None, None]  # noqa: E731   [1, 1, H, N, d]
         kvc.kvc_page_write(self.pg, view(K), view(V), self.slots, self.pool_K, self.pool_V, layer,
                            stream=self.stream)
@@ -121,6 +136,7 @@ class PagedCache:
             raise ValueError("rows is [requests, T] bool")
         if K.shape[0] * K.shape[3] > self._planned:
             raise ValueError("more tokens than were planned")
+        self._take(K, V, rows)
         with torch.cuda.stream(self.stream):
             slots = self.slots
             if rows is not None:
@@ -141,11 +157,25 @@ class PagedCache:
         if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
                                 or lse.device != q.device or not lse.is_contiguous()):
             raise ValueError("lse is [N, n_q_heads] float32, contiguous")
+        self._take(q, out, lse)
         at = kvc.attn_params(q, out, layer, scale, causal, window)
         kvc.kvc_paged_attention(self.pg, at, q, self.pool_K, self.pool_V, self.table, self.q_start,
                                 self.kv_lens, out, self.workspace, self.dev_status, lse=lse,
                                 stream=self.stream)
         return out
+
+    def _take(self, *tensors: Optional[torch.Tensor]) -> None:
+        """A call's tensors belong to the current stream: the cache's own waits for
+        what was given to it, and their memory is not reused before it is done."""
+        if self.stream is None:
+            return
+        current = torch.cuda.current_stream(self.pool_K.device)
+        if current == self.stream:
+            return
+        self.stream.wait_stream(current)
+        for x in tensors:
+            if x is not None:
+                x.record_stream(self.stream)
 
     def _tokens(self, x: torch.Tensor) -> None:
         if x.dim() != 3 or x.shape[0] > self._planned or x.shape[2] != self.pg.d:

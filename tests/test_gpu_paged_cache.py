@@ -77,3 +77,86 @@ def test_context_of_a_memory_lean_chain_between_its_edges():
             if other > 2:
                 with pytest.raises(ValueError):
                     paged.from_chain(lean, other, 8, 5, 16)       # its edge has not run
+
+
+def _steps(stream, busy, lists):
+    """Steps of a cache with and without a stream of its own; every input is made on the
+    current stream behind a pause, dropped or overwritten after its call, and the
+    outputs' memory is handed on at once."""
+    from agent_shared_context_gb300 import paged
+    g = torch.Generator(device="cuda").manual_seed(9)
+    pause = (lambda: torch.cuda._sleep(4_000_000)) if busy else (lambda: None)
+    pause()
+    pc = paged.PagedCache(2, 2, 64, "bf16", 8, 64, 16, 3, 12, 200, stream=stream)
+    kept, dropped = [], []
+    for lens in [[40, 3, 0], [1, 5, 30], [1, 1, 1], [0, -1, 2], [2, 7, 1]] * 2:
+        if stream is not None and busy:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(4_000_000)
+        pause()
+        N = sum(max(n, 0) for n in lens)
+        pc.plan(lens if lists else torch.tensor(lens, dtype=torch.int32).pin_memory().to(
+            "cuda", non_blocking=True), N)
+        for i in range(2):
+            rows = lambda h: torch.randn((N, h, 64), generator=g, device="cuda").bfloat16()  # noqa: E731
+            q, k, v, lse = rows(8), rows(2), rows(2), torch.empty((N, 8), device="cuda")
+            pc.write(i, k, v)
+            kept.append((pc.attend(i, q, lse=lse), lse))
+            pc.attend(i, q)                        # dropped: its memory is the next one's
+            dropped.append(torch.full_like(q, 7.0))
+            del q, k, v
+            junk = [torch.full((N, h, 64), 9.0, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2)]
+            del junk
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in dropped)
+    assert not int(pc.dev_status) and not pc.plan_status.any()
+    return kept, pc
+
+
+@pytest.mark.parametrize("lists", [False, True])
+def test_cache_on_a_stream_of_its_own(lists):
+    want, a = _steps(None, False, lists)
+    for _ in range(3):
+        got, b = _steps(torch.cuda.Stream(), True, lists)
+        for (x, s), (y, t) in zip(want, got):
+            assert torch.equal(x, y) and torch.equal(s, t)
+        assert a.kv_lens.tolist() == b.kv_lens.tolist() == [88, 7, 68]   # 1 ends twice
+        assert torch.equal(a.pool_K, b.pool_K) and torch.equal(a.pool_V, b.pool_V)
+        assert torch.equal(a.table, b.table) and int(a.n_free) == int(b.n_free)
+
+
+def test_context_of_a_chain_on_a_stream_of_its_own():
+    from agent_shared_context_gb300 import paged, synth
+    from agent_shared_context_gb300.chain import ChainRunner
+    wl = synth.scaled(synth.workload("llama2k"), L=2, H=2, R=2, seg_len=[64, 72], pf=24)
+    inp = synth.generate(wl, device="cuda")
+    side = torch.cuda.Stream()
+    want = ChainRunner(wl, inp)
+    want.run()
+    for keep in (True, False):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            runner = ChainRunner(wl, inp, stream=side, keep_outputs=keep)
+            torch.cuda._sleep(20_000_000)
+        runner.run()
+        pc = paged.from_chain(runner, 3, 8, 5, 16)             # the current stream is idle
+        side.synchronize()
+        for r in range(wl.R):
+            for x, held in zip((pc.pool_K, pc.pool_V), want.held(3)):
+                assert torch.equal(_rows(pc, x, r, wl.T), held[r])
+
+
+def test_captured_steps_take_no_list():
+    pc = _cache()
+    pc.plan([1, 1, 1], 3)
+    graph = torch.cuda.CUDAGraph()
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        with pytest.raises(ValueError):
+            pc.plan([1, 1, 1], 3)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [1] * 4 and pc.kv_lens.tolist() == [1] * 3
