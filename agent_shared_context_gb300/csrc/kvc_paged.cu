@@ -241,11 +241,11 @@ kvc_status kvc_page_write(const kvc_paged* pg, int32_t n_src, int32_t T, int32_t
   if (static_cast<int64_t>(n_layers) * pg->H > 65535)
     return fail(KVC_ERR_UNSUPPORTED, "n_layers * H = %lld exceeds 65535",
                 static_cast<long long>(n_layers) * pg->H);
-  KVC_TRY(check_view(pg, src_K, "src_K"));
-  KVC_TRY(check_view(pg, src_V, "src_V"));
   KVC_TRY(check_pool(pg, pool_K, "pool_K"));
   KVC_TRY(check_pool(pg, pool_V, "pool_V"));
-  if (n_src == 0 || T == 0) return KVC_OK;
+  if (n_src == 0 || T == 0) return KVC_OK;           // sources of no rows may have no address
+  KVC_TRY(check_view(pg, src_K, "src_K"));
+  KVC_TRY(check_view(pg, src_V, "src_V"));
   KVC_TRY(check_ptr(slot_map, "slot_map", 8));
   const Span pools[2] = {view_span(pg, pool_K, pg->n_pages, pg->L, pg->page_size),
                          view_span(pg, pool_V, pg->n_pages, pg->L, pg->page_size)};

@@ -476,7 +476,8 @@ kvc_status kvc_page_plan(const kvc_paged* pg, const int32_t* new_lens, const int
  *
  * src_K, src_V are views [n_src, n_layers, H, T, d]; token t of source r goes
  * to slot_map[r * T + t] of layers [layer, layer + n_layers) of the pools.
- * Tokens whose slot is outside [0, P B) are skipped.  New tokens of one layer,
+ * Tokens whose slot is outside [0, P B) are skipped; with n_src or T 0 neither
+ * the sources nor slot_map need be there.  New tokens of one layer,
  * packed [N, H, d], are a view with n_src = n_layers = 1 and T = N; a chain's
  * corrected caches [R, L, H, T, d] are views as they are.  Two tokens with the
  * same slot race.  The pools may not overlap the sources.  n_layers * H <=

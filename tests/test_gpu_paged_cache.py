@@ -160,3 +160,20 @@ def test_captured_steps_take_no_list():
     graph.replay()
     torch.cuda.synchronize()
     assert x.tolist() == [1] * 4 and pc.kv_lens.tolist() == [1] * 3
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_steps_without_tokens(dtype):
+    pc = _cache(dtype)
+    dt = pc.pool_K.dtype
+    pc.plan([5, 0, 3], 8)
+    q = torch.randn((8, 8, 64), device="cuda").to(dt)
+    pc.write(1, q[:, :2], q[:, 2:4])
+    K = pc.pool_K.clone()
+    pc.plan([0, 0, 0], 0)
+    pc.write(1, q[:0, :2], q[:0, 2:4])
+    assert pc.attend(1, q[:0]).shape == (0, 8, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(K, pc.pool_K) and pc.kv_lens.tolist() == [5, 0, 3]
+    assert pc.q_start.tolist() == [0] * 4
+    assert not int(pc.dev_status) and not pc.plan_status.any()

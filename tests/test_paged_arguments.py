@@ -79,3 +79,17 @@ def test_plan_refuses_lengths_elsewhere(pc):
     for bad in (torch.zeros(2, dtype=torch.int32, device="meta"), torch.zeros(2, dtype=torch.int64),
                 torch.zeros((2, 1), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)):
         _refused(pc.plan, bad)
+
+
+def test_writing_nothing_takes_empty_tensors():
+    """An empty tensor has no address."""
+    from agent_shared_context_gb300 import kvc
+    pg = kvc.paged(16, 8, 2, 4, 64, "bf16", 2, 4)
+    pool = kvc.cache_view(0x7F0000000000, (2 * 4 * 8 * 64, 4 * 8 * 64, 8 * 64, 64))
+    for shape in ((0, 2, 4, 3, 64), (2, 2, 4, 0, 64)):
+        x = torch.zeros(shape, dtype=torch.bfloat16)
+        assert kvc.kvc_page_write(pg, x, x, None, pool, pool, stream=0) == kvc.KVC_OK
+        with pytest.raises(kvc.KvcError):          # the rest is looked at all the same
+            kvc.kvc_page_write(pg, x, x, None, kvc.cache_view(None), pool, stream=0)
+        with pytest.raises(kvc.KvcError):
+            kvc.kvc_page_write(pg, x, x, None, pool, pool, layer=1, stream=0)
