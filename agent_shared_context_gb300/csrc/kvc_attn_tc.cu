@@ -436,7 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         it.ntiles = 0;
       int edge_lo = 0, edge_hi = 0;
-      if (more) edges(p.s, sight(a, it.kv, it.pos0, it.nt), &edge_lo, &edge_hi);
+      Sight see{};
+      if (more) {
+        see = sight(a, it.kv, it.pos0, it.nt);
+        edges(p.s, see, &edge_lo, &edge_hi);
+      }
       if (lane == 0) {
         b->items[slot].it = it;
         b->items[slot].ring0 = ring;
@@ -449,14 +453,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool pair = it.nt > p.tok_tile;
 
       // Page and first row in it of the lane's box of key tiles 0, 1, ... in order,
-      // looked up one tile ahead.  A box beyond the pool (page P) is filled with 0.
+      // looked up one tile ahead.  A box beyond the pool (page P) is filled with 0, as is
+      // one that no row sees: its page may not be the request's any more.
       const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
       struct Box {
         int page, row;
       };
       auto fetch = [&](int tile) -> Box {
         const int tok = tile_span(p, tile).tok0 + my_run * p.run_tokens;
-        if (lane >= boxes || tok >= it.kv) return Box{kNoPage, 0};
+        if (lane >= boxes || tok >= see.any_hi || tok + p.run_tokens <= see.any_lo)
+          return Box{kNoPage, 0};
         const int blk = fast_div(tok, p.page);
         return Box{table[blk], tok - blk * a.B};
       };

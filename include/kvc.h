@@ -531,9 +531,10 @@ typedef struct kvc_attn_params {
  * overlap on the GPU need workspaces of their own.  Results do not depend on
  * the order in which CTAs finish.
  *
- * *dev_status becomes KVC_ERR_SHAPE if the lengths, q_start or a page index
- * in use are out of range (lengths are clamped, the rows of such a page count
- * as zeros), KVC_ERR_DEVICE_TIMEOUT if a bounded device wait expired (zero
+ * *dev_status becomes KVC_ERR_SHAPE if the lengths, q_start or the page index of
+ * a key that some row sees are out of range (lengths are clamped, the rows of such
+ * a page count as zeros; entries of keys behind every row's window mean nothing),
+ * KVC_ERR_DEVICE_TIMEOUT if a bounded device wait expired (zero
  * the workspace before its next use).
  * ------------------------------------------------------------------------- */
 size_t kvc_paged_attention_workspace(const kvc_paged* pg, const kvc_attn_params* at);

@@ -99,3 +99,29 @@ def test_windows_longer_than_any_context(dtype, d, G, window, lens):
     b = Batch(lens, 2 * G, 2, d, 16, dtype, seed=G)
     b.run(True, window)
     b.check(True, window)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("B", [8, 16, 48, 130])
+@pytest.mark.parametrize("lens", [[(1, 900), (2, 700), (0, 5), (1, 50)],
+                                  [(40, 900), (1, 700), (150, 800), (3, 40)]],
+                         ids=["few", "chunks"])
+def test_pages_behind_the_window_are_not_in_use(dtype, d, B, lens):
+    """A serving program may give them back: their entries mean nothing."""
+    window = 100
+    b = Batch(lens, 4, 2, d, B, dtype, seed=B)
+    gone = 0
+    for r, (n, kv) in enumerate(lens):
+        first = max(0, kv - n - window + 1) if n else kv          # the first key that a row sees
+        for k, junk in zip(range(first // B), [-1, b.P, 2 ** 31 - 1, -2 ** 31] * 30):
+            b.d_table[r, k] = junk
+            gone += 1
+    assert gone > 5
+    b.run(True, window)
+    b.check(True, window)                          # with the status
+    # an entry in sight is reported
+    b.d_table[0, (lens[0][1] - 1) // B] = b.P
+    b.run(True, window)
+    torch.cuda.synchronize()
+    from agent_shared_context_gb300 import kvc
+    assert int(b.status.item()) == kvc.KVC_ERR_SHAPE
