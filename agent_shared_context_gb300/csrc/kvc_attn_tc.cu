@@ -181,14 +181,31 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars<N
   return wait_on(bar, parity, &b->abort_flag);
 }
 
-// A whole warp waits until *count, which another warp raises, has reached `want`.
-__device__ __noinline__ bool warp_wait_count(const volatile int32_t* count, int32_t want,
+// A count that one thread raises after it has seen something land, and that others
+// wait for: what was visible to the one that raised it is visible to them.
+__device__ __forceinline__ void raise_count(int32_t* count) {
+  const uint32_t at = smem_u32(count);
+  asm volatile(
+      "{\n\t.reg .b32 n;\n\t"
+      "ld.relaxed.cta.shared::cta.b32 n, [%0];\n\t"
+      "add.s32 n, n, 1;\n\t"
+      "st.release.cta.shared::cta.b32 [%0], n;\n\t}" ::"r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ int32_t read_count(const int32_t* count) {
+  int32_t n;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
+  return n;
+}
+
+// A whole warp waits until *count has reached `want`.
+__device__ __noinline__ bool warp_wait_count(const int32_t* count, int32_t want,
                                              volatile int32_t* abort) {
   Patience p;
   bool ok = true;
 #pragma unroll 1
-  while (ok && *count - want < 0) ok = !p.out(abort);
-  __threadfence_block();
+  while (ok && read_count(count) - want < 0) ok = !p.out(abort);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -598,10 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pv) {
           ok = own(v_at);
           if (!ok) break;
-          if (lane == 0) {
-            volatile int32_t* landed = &b->landed[st];
-            *landed = *landed + 1;
-          }
+          if (lane == 0) raise_count(&b->landed[st]);
         }
         if (more) ok = own(k_at);
         if (!ok) break;
@@ -710,8 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sH = sS + half * kHalf;
         const uint32_t* bad = nullptr;                      // value rows that are added from memory
         if (edge) {
-          const int slot_v = (ring0 + ring_v(pair, it.ntiles, i)) % NS;
-          ok = warp_wait_count(&b->landed[st], n_tiles + k + 1, &b->abort_flag);
+          // The count says that the barrier's phase is the tile's (a wait on a parity alone
+          // could pass one phase early); it stays so until the tile is given back, after
+          // these rows' P.  The wait itself then makes the copy's bytes visible here.
+          const int ring_pos = ring0 + ring_v(pair, it.ntiles, i), slot_v = ring_pos % NS;
+          ok = warp_wait_count(&b->landed[st], n_tiles + k + 1, &b->abort_flag) &&
+               warp_wait(&b->kv_full[slot_v], (ring_pos / NS) & 1, b);
           if (!ok) break;
           const TileSpan t = tile_span(p, it.tile0 + i);
           const Sight see = sight(a, it.kv, it.pos0, it.nt);

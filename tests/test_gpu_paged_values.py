@@ -125,3 +125,34 @@ def test_pages_behind_the_window_are_not_in_use(dtype, d, B, lens):
     torch.cuda.synchronize()
     from agent_shared_context_gb300 import kvc
     assert int(b.status.item()) == kvc.KVC_ERR_SHAPE
+
+
+@pytest.mark.parametrize("d,B", [(64, 16), (128, 16), (128, 48), (64, 130)])
+@pytest.mark.parametrize("window", [130, 400])
+def test_infinities_along_a_window(d, B, window):
+    """One key in thirty holds an infinity, so that most tiles at the edges of sight have
+    value rows that some rows see and others do not; call after call with the same bits."""
+    lens = [(700, 3000), (150, 900), (33, 300), (1, 500)]
+    G = 4
+    b = Batch(lens, 2 * G, 2, d, B, "bf16", seed=B)
+    rng = np.random.RandomState(d + B)
+    plus = np.zeros((b.N, 2 * G, d), dtype=bool)
+    for r, (n, kv) in enumerate(lens):
+        for j in np.flatnonzero(rng.rand(kv) < 1 / 30):
+            page, row = _key(b, r, j)
+            head, col = rng.randint(2), rng.randint(d)
+            b.host[1][page, 0, head, row, col] = 0.0
+            b.V[page, 0, head, row, col] = float("inf")
+            plus[_sees(b, r, j, True, window), head * G:head * G + G, col] = True
+    plus = torch.from_numpy(plus).cuda()
+    assert 0.01 < plus.float().mean() < 0.5
+    b.run(True, window)
+    got = b.out.clone()
+    assert (got[plus] == float("inf")).all()
+    for _ in range(20):
+        b.run(True, window)
+        assert torch.equal(got, b.out)
+    b.V.copy_(b.host[1])
+    b.run(True, window)
+    b.out.copy_(torch.where(plus, b.out, got))
+    b.check(True, window)
