@@ -12,7 +12,8 @@
 // and x y = h h' + h e' + e h' up to 5 2^-22 |x y| (the cut 2^-21 of each, and
 // e e').  The tensor core's sums may drop bits where an FMA would round, so no
 // sum of theirs is longer than a tile: a tile's P V is added to O by an FMA.
-// Numbers below 2^-115 keep the 11 bits of h alone.
+// Numbers from 2^-126 to 2^-115 keep the 11 bits of h alone (e is below the smallest
+// normal number), smaller ones may count as zeros.
 //
 // A row is (token, query head of the KV head's group), so that K and V are read
 // once for the whole group.  Eight warps: RB groups of rows, of MB blocks of 16,

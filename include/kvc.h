@@ -523,7 +523,8 @@ typedef struct kvc_attn_params {
  * key carries much of its row; up to 128 rows of no more tokens than requests run
  * in a decoding kernel on warp-level tensor-core instructions, with two numbers.
  * f32 runs on these with every factor split into two tf32 numbers: a product
- * is off by at most 5 2^-22 of itself (by 2^-10 for factors below 2^-115).
+ * is off by at most 5 2^-22 of itself, by 2^-10 with a factor below 2^-115, and
+ * factors below 2^-126 may count as zeros.
  *
  * `workspace` holds kvc_paged_attention_workspace() bytes (0 for descriptors
  * that the call would refuse), 256-byte aligned.  ITS FIRST 8,192 BYTES MUST

@@ -8,6 +8,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged_oracle as PO
+
 from .test_gpu_paged import FEW, Batch
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +158,30 @@ def test_infinities_along_a_window(d, B, window):
     b.run(True, window)
     b.out.copy_(torch.where(plus, b.out, got))
     b.check(True, window)
+
+
+@pytest.mark.parametrize("lens", [FEW, CHUNKS], ids=["few", "chunks"])
+@pytest.mark.parametrize("low,high", [(-125, -116), (-149, -127)])
+def test_f32_tiny_factors(lens, low, high):
+    """Keys of 2^low .. 2^high.  From 2^-126 on a product is off by at most 2^-10 of
+    itself, and smaller factors may count as zeros: a score is off by 2^-10 E, or by E,
+    besides what it is off by elsewhere."""
+    b = Batch(lens, 4, 2, 64, 16, "f32", seed=8)
+    g = torch.Generator().manual_seed(2)
+    K, q = b.host[0], b.host[2]
+    size = torch.exp2(torch.rand(K.shape, generator=g, dtype=torch.float64) * (high - low) + low)
+    K.copy_(torch.where(K.isnan(), K, torch.copysign(size.float(), K)))
+    q.mul_(2.0 ** 119)
+    b.K.copy_(K), b.q.copy_(q)
+    b.run()
+    n64 = lambda t: t.double().numpy()  # noqa: E731
+    o, z, A, E = PO.paged_attention(n64(q), n64(K), n64(b.host[1]), b.table, b.q_start,
+                                    [kv for _, kv in lens], 64 ** -0.5)
+    torch.cuda.synchronize()
+    n = max(kv for _, kv in lens)
+    ds = ((2.0 ** -10 if low >= -126 else 1.0) + (64 + 16) * 2.0 ** -24) * E
+    off = np.abs(b.out.cpu().double().numpy() - o)
+    assert (off <= (np.expm1(2 * ds[:, :, None]) + (n + 4) * 2.0 ** -24) * A
+            + 2.0 ** -23 * np.abs(o)).all()
+    off = np.abs(b.lse.cpu().double().numpy() - z)
+    assert (off <= ds + (n + 4) * 2.0 ** -24 + 2.0 ** -23 * np.abs(z)).all()
