@@ -105,8 +105,11 @@ __device__ __forceinline__ int n_items(const SchedArgs& a, const Request& q) {
   return fast_div(q.nq + a.item.d - 1, a.item);
 }
 
-// sum over 0 <= i < n of floor((a i + b) / m), by the steps of Euclid's
-// algorithm on (a, m).
+// sum over 0 <= i < n of floor((a i + b) / m): the lattice points under a line (on sums
+// of floors: Graham, Knuth and Patashnik, "Concrete Mathematics", 3.5).  The whole parts
+// of a / m and b / m are summed in closed form; of what is left the points are counted
+// by rows in place of columns, a sum of the same kind with a and m exchanged, so that
+// (a, m) goes the way of Euclid's algorithm.
 static __device__ __noinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t s = 0;
   while (n > 0) {
