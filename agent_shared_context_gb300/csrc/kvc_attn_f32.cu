@@ -179,8 +179,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DC, RB, MB>::kCtasSm)
     const int rows = it.nt * a.G;
     const int all_hi = a.causal ? min(it.kv, it.pos0 + 1) : it.kv;      // keys that all rows see
     const int all_lo = a.window > 0 ? max(0, it.pos0 + it.nt - a.window) : 0;
-    const int any_hi = a.causal ? min(it.kv, it.pos0 + it.nt) : it.kv;  // and that any row sees
-    const int any_lo = a.window > 0 ? max(0, it.pos0 + 1 - a.window) : 0;
 
     const int32_t* table = a.table + static_cast<int64_t>(it.r) * a.width;
     // where the rows of tile t lie
@@ -189,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DC, RB, MB>::kCtasSm)
       if (kv > 1 || t >= it.ntiles) return;
       const int tok = (it.tile0 + t) * kTile + n;
       int64_t off = -1;
-      if (tok >= any_lo && tok < any_hi) {
+      // keys that some row sees: others' pages may not be the request's any more
+      if (tok < (a.causal ? min(it.kv, it.pos0 + it.nt) : it.kv) &&
+          (a.window == 0 || tok > it.pos0 - a.window)) {
         const int blk = fast_div(tok, per_page);
         const int page = table[blk];
         if (page >= 0 && page < a.P)
