@@ -25,9 +25,9 @@
 //
 // Measured, 32 query heads on 8 of 128: 16 requests of 10,240 keys 109 us, 671 MB at
 // 6.2 TB/s (asymptotically 7.2 TB/s and some 10 us of launch, division of the work,
-// first loads and joining); one request of 131,072 keys 88 us, 6.1 TB/s; one of 777
-// keys 9.5 us, all of it latency.  Where the chunk kernel would be faster: launch
-// rules below.
+// first loads and joining); one request of 131,072 keys 87 us, 6.1 TB/s; one of 777
+// keys 9.0 us, all of it latency.  Of 64: 16 requests of 10,240 keys 61 us, 5.5 TB/s.
+// Where the chunk kernel would be faster: launch rules below.
 #include <cuda_bf16.h>
 
 #include "kvc_attn_sched.cuh"

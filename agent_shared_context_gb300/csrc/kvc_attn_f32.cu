@@ -30,15 +30,16 @@
 // element by element in FP32.
 //
 // Measured, in us, with FP32 FMAs in place of the tensor cores in brackets: four
-// chunks of 300 tokens over 4,000 keys, 8 on 2 heads, of 64: 236 (338), 40 TFLOP/s
-// of the 9.5 GFLOP that count; of 128: 420 (685); decoding 16 requests of 5,000
-// keys with heads of 128: 71 (199), 2.3 TB/s; six ragged chunks of up to 65 tokens
-// over 2,000 keys, heads of 64: 28 (41).  (FMAs were bound by their rate and by
+// chunks of 300 tokens over 4,000 keys, 8 on 2 heads, of 64: 239 (338), 40 TFLOP/s
+// of the 9.5 GFLOP that count; of 128: 417 (685); decoding 16 requests of 5,000
+// keys with heads of 128: 67 (199), 2.4 TB/s; six ragged chunks of up to 65 tokens
+// over 2,000 keys, heads of 64: 27 (41).  (FMAs were bound by their rate and by
 // shared memory.)  The tensor cores alone would take 95 us for the first: there is
 // room for two warps a scheduler, 255 registers each, and they wait for one
 // another's chains (issue slots 43%, tensor pipe 40% busy).  Two blocks of 16 rows
 // in a warp share the splitting of K and V: with one block, 16 warps an SM, the
-// first took 271 us.
+// first took 271 us.  Decoding has two tiles of copies in flight, and the next ones
+// start when all warps have searched a tile and met: 0.36 of HBM's rate.
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
 

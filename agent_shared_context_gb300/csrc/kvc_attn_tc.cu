@@ -47,16 +47,22 @@
 // as two numbers, cut_bf16 and the rest of it: few steps of a long context.  S
 // leaves room for the rest in TMEM, beside P.
 //
+// Error against 64 bits (root of the mean square), beside that of f32 arithmetic
+// rounded once: the dense prefill below 2.50e-4 (2.25e-4), the sixteen chunks 1.41e-4
+// (1.13e-4).  Two numbers from 1/16 on would give 2.39e-4 and 1.33e-4 and take 1,026
+// and 335 us; in every step the error in brackets, and 1,241 and 405 us.
+//
 // Measured: dense prefill of two contexts of 8,192 tokens, 32 query heads on 8 of 128,
-// 0.97 ms, 1.14 PFLOP/s or 0.60 of the library's matrix products; sixteen chunks of 128
-// tokens over 10,368 keys 320 us, 1.08 PFLOP/s; five ragged ones of up to 700 tokens,
-// 28 on 4 heads, a window of 4,096, pages of 48: 105 us, 0.59 PFLOP/s.  A pair of row
-// tiles takes some 3,800 cycles per 128 keys, of which the MMAs need 2,500: with both
-// operands of S = Q K^T in shared memory (TMEM is full: S and O of two streams) a step
-// of 16 columns takes 90 cycles instead of 64 for reading them, and each half of a tile
-// waits for the softmax's and the MMA's signals.  An item costs some 10,000 cycles
-// besides (masked tiles, the output), a CTA 5 us to its first tile, a divided item's
-// end 8 us.
+// 0.96 to 0.97 ms, 1.14 PFLOP/s or 0.60 of the library's matrix products; sixteen chunks
+// of 128 tokens over 10,368 keys 320 us, 1.08 PFLOP/s (heads of 64: 253 us, 0.68
+// PFLOP/s); five ragged ones of up to 700 tokens, 28 on 4 heads, a window of 4,096, pages
+// of 48: 104 us, 0.59 PFLOP/s.  A pair of row tiles takes some 3,800 cycles per 128 keys.
+// A loop of its MMAs alone takes 2,960 of these: a step of 16 columns of S for 64 keys
+// 60 cycles, hardly less than the 65 that one for 128 keys takes, since both read all of
+// Q's columns out of shared memory (with Q in TMEM 48); a step of P V 64.  At the full
+// rate the MMAs would need 2,050.  The rest is the hand-over: each half of a tile waits
+// for the softmax's and the MMA's signals.  An item costs some 10,000 cycles besides
+// (masked tiles, the output), a CTA 5 us to its first tile, a divided item's end 8 us.
 //
 // Every wait is bounded: one that expires stores KVC_ERR_DEVICE_TIMEOUT into
 // *dev_status and raises the CTA's abort flag; the roles stop, copies and MMAs

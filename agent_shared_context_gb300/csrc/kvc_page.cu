@@ -17,8 +17,8 @@
 //
 // Bound by launch and L2 latency for a step of a few requests, by the 12 bytes
 // written per token for large admissions.  Measured: 16 requests with a token each
-// 5.4 us, most of it the host's; 1,024 requests of which 100 end and the rest bring
-// up to 1,024 tokens each, 465,000 in all, 9.0 us (5.8 MB: 0.86 us of HBM time; the
+// 5.5 us, most of it the host's; 1,024 requests of which 100 end and the rest bring
+// up to 1,024 tokens each, 465,000 in all, 8.8 us (5.8 MB: 0.86 us of HBM time; the
 // sums over the requests and the search of each run of tokens are the rest).
 #include "kvc_attn_sched.cuh"
 #include "kvc_paged_internal.h"
@@ -306,7 +306,8 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const size_t smem = static_cast<size_t>(a.R) * kPlanBytes;
   // Four tokens to a thread, with 16-byte stores, once every thread of the GPU has more
-  // than one: 8.4 against 6.2 us for 16 tokens, 12.8 against 15.9 us for 470,000.
+  // than one: in a replayed graph 4.1 against 3.4 us for 16 tokens, 8.8 against 10.4 us
+  // for 465,000.
   const bool vec = a.max_tokens > di.sm_count * kPlanThreads &&
                    (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0;

@@ -516,7 +516,8 @@ typedef struct kvc_attn_params {
  * decoding; requests with one token, with many and with none may be mixed.
  * An infinite value gives the rows that see it an infinity of its sign, NaN beside
  * one of the other sign; where its weight is below 2^-90 of the row's largest it may
- * be left out or give NaN.
+ * be left out or give NaN.  The sums of p v are divided by those of p at the end:
+ * values above 2^90 may overflow them.
  * Rows of no request are not written.  All sums, maxima and the softmax
  * are fp32.  bf16: chunks run on tcgen05 tensor cores, with the probabilities
  * rounded to bf16 for the product with V, or as two bf16 numbers (16 bits) where a
