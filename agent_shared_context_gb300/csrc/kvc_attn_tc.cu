@@ -72,11 +72,15 @@
 //                   make Q fp16 in place, times a power of two for each row.
 // 32 neighbouring keys share one exponent of K, which goes into their scores, and one of
 // V, which goes into the exponents of P: nothing is multiplied key by key unless exponents
-// are more than 15 apart.  P is fp16 relative to the largest term of O, not of l; its 11
-// bits need no second number.  The largest term is 2^5 when m is set and may grow to 2^15:
-// with 2^12 (terms good to 2^-37 of it, not 2^-30) O is rescaled oftener, 454 us.
-// Measured: sixteen chunks of 128 tokens over 10,368 keys, blocks of 16, 428 us, 0.81
-// PFLOP/s (bf16 pools 323); five ragged ones, a window of 4,096, pages of 48, 128 us (105).
+// of K are more than 15 apart or those of V more than 10.  P is fp16 relative to the
+// largest term of O, not of l; its 11 bits need no second number.  With a shared exponent a
+// term may look larger than it is by as much as V's exponents differ, so where m is set the
+// largest is 2^5 times that, for the true one to be 2^5 at least; it may grow to 2^15.  With
+// 2^12 (terms good to 2^-37 of the largest, not 2^-30) O is rescaled oftener, 454 us.
+// Measured: sixteen chunks of 128 tokens over 10,368 keys, blocks of 16, 438 us, 0.79
+// PFLOP/s (bf16 pools 323); five ragged ones, a window of 4,096, pages of 48, 132 us (105).
+// Without regard to how far V's exponents differ 428 and 128 us, and terms good to 2^-15 of
+// the largest only.
 // A pair of row tiles takes some 6,000 cycles for 128 keys, a half 3,000: 420 to its
 // first scores, 560 for their largest, 1,120 for P, the rest rescales and waits.  512
 // threads leave it 128 registers and a fourth warp in each quarter of the SM: 3,300
@@ -121,6 +125,9 @@ constexpr int kItemCost = 6;               // tiles that an item's beginning and
 constexpr float kLag = 8.0f;               // log2 by which m may lag behind
 constexpr float kRoom = 15.0f;             // log2 of P's largest value as fp16
 constexpr float kTop = 5.0f;               // and of that of the largest term when m is set
+constexpr int kSpanK = 15, kSpanV = 10;    // most by which exponents of 32 keys with one differ
+constexpr uint32_t kOwn = 0x80;            // ScaledInfo: keys with exponents of their own
+static_assert(kTop + kSpanV <= kRoom, "the largest term when m is set fits P");
 constexpr float kApart = 60.0f;            // exponents of V that are looked at key by key
 constexpr float kFar = 90.0f;              // log2 from where a larger score counts all others out
 constexpr float kHeavyPair = 0.125f;       // share of a row's sum that makes a key heavy
@@ -186,10 +193,10 @@ template <int DEPTH>
 struct ScaledInfo {
   // Of each 32 keys of a tile, at the ring position of its K modulo DEPTH (twice the slots:
   // a stream looks at it before it gives the tile's V back): K's power of two, the exponent
-  // of V's and that power's inverse, and whether the keys have exponents of their own instead.
+  // of V's and that power's inverse, and by how much V's exponents differ, or kOwn.
   struct alignas(8) Tile {
     float k[4], v_exp[4], v_inv[4];
-    uint8_t wide[4];
+    uint8_t span[4];
   } tile[DEPTH];
   int8_t q_up[2][2 * kRowsM];      // rows of Q are times 2^q_up, of this item and the next
   uint64_t q_ready;                // Q is fp16
@@ -431,15 +438,14 @@ __device__ __forceinline__ float score_scale(float row_scale, float k) {
 // The exponent byte of a power of two.
 __device__ __forceinline__ int exp_byte(float x) { return __float_as_int(x) >> 23; }
 
-// The largest exponent byte of a warp's keys (a lane has one, those in `rows` count);
-// *wide is set where another one is more than 15 below, those of the least
-// exponent (of blocks of zeros) aside.
-__device__ __forceinline__ int group_exp(int exp, uint32_t rows, bool* wide) {
+// The largest exponent byte of a warp's keys (a lane has one, those in `rows` count), and by
+// how much another one of at least `from` is below.
+__device__ __forceinline__ int group_exp(int exp, uint32_t rows, int from, int* span) {
   const bool has = (rows >> (threadIdx.x & 31)) & 1u;
   const uint32_t top = __reduce_max_sync(0xffffffffu, has ? static_cast<uint32_t>(exp) : 0u);
-  const uint32_t low = __reduce_min_sync(
-      0xffffffffu, has && exp > kScaleExpMin + 127 ? static_cast<uint32_t>(exp) : 255u);
-  if (low < 255u && top > low + 15u) *wide = true;
+  const uint32_t low =
+      __reduce_min_sync(0xffffffffu, has && exp >= from ? static_cast<uint32_t>(exp) : 255u);
+  *span = max(static_cast<int>(top) - static_cast<int>(low), 0);
   return static_cast<int>(top);
 }
 
@@ -983,9 +989,12 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
             // Keys with exponents of their own, or so far apart that sums of the smaller terms
             // would not be seen by those of the weights, are taken one by one.
             const float2 v_exp = *reinterpret_cast<const float2*>(&info.v_exp[2 * half]);
-            const uint32_t flags = *reinterpret_cast<const uint16_t*>(&info.wide[2 * half]);
+            auto spans = [&]() -> uint32_t {
+              return *reinterpret_cast<const uint16_t*>(&info.span[2 * half]);
+            };
             v_top = max3(v_top, v_exp.x, v_exp.y);
-            const bool apart = (fminf(v_exp.x, v_exp.y) < v_top - kApart) | (flags != 0);
+            const bool apart = (fminf(v_exp.x, v_exp.y) < v_top - kApart) |
+                               ((spans() & (kOwn | kOwn << 8)) != 0);
             uint32_t x[32];
             auto scores = [&](int g) {
               tmem_ld_32x32b_x32(sH + 32 * g, x);
@@ -1000,7 +1009,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
             auto sc = [&](int j) { return __uint_as_float(x[j]); };
             // exponent bytes of key `lane` of group g, V's above K's
             auto own_exps = [&](int g) {
-              if (!info.wide[2 * half + g])
+              if (info.span[2 * half + g] != kOwn)
                 return exp_byte(info.k[2 * half + g]) |
                        static_cast<int>(info.v_exp[2 * half + g] + 127.f) << 8;
               return exps_of(p, it, sight(a, it.kv, it.pos0, it.nt),
@@ -1039,7 +1048,10 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
             }
             const bool raise = top > m + kRoom || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, raise)) {
-              const float m_new = raise ? top - kTop : m;
+              // a term may be smaller than `top` says by its group's span
+              const uint32_t two = spans();
+              const uint32_t span = max(two & (kOwn - 1), (two >> 8) & (kOwn - 1));
+              const float m_new = raise ? top - (kTop + static_cast<float>(span)) : m;
               const float f = raise ? exp2_fast(m - m_new) : 1.f;            // 0 from m = -inf
               // l may have what m lacks: in two steps
               const float h = raise ? exp2_fast(0.5f * (m - m_new)) : 1.f;
@@ -1251,7 +1263,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
                 const int g = 2 * half + (n >> 5);
                 const int e = p.sc.exps[1][page * p.sc.s_page + a.layer * p.sc.s_layer +
                                            it.h * p.sc.s_head + fast_div(tok - blk * a.B, p.block)];
-                if (!info.wide[g])
+                if (info.span[g] != kOwn)
                   v_scale = pow2_of(max(e - static_cast<int>(info.v_exp[g]), 0));
               }
               auto value = [&](int c) {
@@ -1543,7 +1555,8 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
       };
       Staged staged[kMost<C::kStages, 1>] = {};    // of the tiles in the stages
       int s = 0, st = 0, empty = C::kStages, ring = 0, n_q = 0;
-      int group_k = 127, group_v = 127, wide = 0;
+      int group_k = 127, group_v = 127, span_v = 0;
+      bool wide = false;
       uint32_t down_v = 0, down_before = 0;        // multipliers of V's rows
       uint32_t wrap = 1;
 #pragma unroll 1
@@ -1558,16 +1571,18 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
           break;
         const bool is_v = (now_in.kind & 3) == 2, is_k = (now_in.kind & 3) == 1;
         // The 32 keys get one exponent, the largest of theirs, and the numbers of the others
-        // are divided by what is between: exact in fp16 up to 2^15.  With more between (least
-        // exponents, of zeros or next to it, aside) all stay as they are and say so.
+        // are divided by what is between: exact in fp16 up to 2^15.  With more between all stay
+        // as they are and say so; of K, the least exponents (of zeros or next to it) aside, and
+        // of V from 2^10 on, for m's sake.
         uint32_t down = now_in.kind & kOld ? down_before : down_v;
         if (is_k) {
-          wide = 0;
+          span_v = 0;
+          wide = false;
           if (now_in.rows != 0) {                  // (none: as the keys before)
-            bool apart = false;
-            group_k = group_exp(now_in.exp_k, now_in.rows, &apart);
-            group_v = group_exp(now_in.exp_v, now_in.rows, &apart);
-            wide = apart;
+            int span_k;
+            group_k = group_exp(now_in.exp_k, now_in.rows, kScaleExpMin + 128, &span_k);
+            group_v = group_exp(now_in.exp_v, now_in.rows, 0, &span_v);
+            wide = span_k > kSpanK || span_v > kSpanV;
           }
           down_before = down_v;
           down_v = f16x2_down(wide ? 0 : group_v - now_in.exp_v);
@@ -1596,7 +1611,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsScaled : kTcThreads, 1)
           info.k[warp - 12] = pow2_of(group_k);
           info.v_exp[warp - 12] = static_cast<float>(group_v - 127);
           info.v_inv[warp - 12] = pow2_of(254 - group_v);
-          info.wide[warp - 12] = static_cast<uint8_t>(wide);
+          info.span[warp - 12] = static_cast<uint8_t>(wide ? kOwn : span_v);
         }
         // 64 columns to a swizzled tile
         const int half = unit >> 2, c = (unit & 3) * 2;

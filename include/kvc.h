@@ -667,9 +667,9 @@ kvc_status kvc_page_write_scaled(const kvc_paged* pg, const kvc_scales* sc, int3
  * scores, V's in the weights, which are rounded to fp16: by 2^-11 of themselves, or by
  * 2^-30 of the largest weight times power of two (times 2^-90 at least) of its row.
  * Chunks bring the numbers of 32 neighbouring keys (from a multiple of 32 on) to one
- * exponent, exactly where theirs differ by up to 15, and take those that differ by more
- * key by key; beside others, blocks of exponent -100 (of zeros, or of elements below
- * 2^-91) may count as zeros.  Keys whose weight is below 2^-90 of the row's largest may
+ * exponent, exactly where K's differ by up to 15 and V's by up to 10, and take those that
+ * differ by more key by key; beside others, K's blocks of exponent -100 (of zeros, or of
+ * elements below 2^-91) may count as zeros.  Keys whose weight is below 2^-90 of the row's largest may
  * be left out.  A NaN in sight gives NaN.
  * The workspace follows the same rules, with its own size.
  * ------------------------------------------------------------------------- */
