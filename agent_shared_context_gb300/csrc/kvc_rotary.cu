@@ -234,26 +234,62 @@ cudaError_t launch(const RotaryArgs& a, int64_t N, bool inter, cudaStream_t stre
   return launch_early(fn, grid, threads, 0, stream, a);
 }
 
-// The bytes of [N, heads, d] rows.
+// The bytes of [N, heads, d] rows, `step` bytes from a token (0) or head (1) to the next.
 struct Extent {
   Span s;
-  int64_t tok, foot;         // bytes from a token to the next, of one token's rows
+  int64_t row, step[2], count[2];
+  // from the first to the last byte of what one token (head) has
+  int64_t foot(int dim) const { return (count[1 - dim] - 1) * step[1 - dim] + row; }
 };
 
 Extent extent(const void* p, int64_t N, int64_t heads, int64_t s_tok, int64_t s_head, int64_t d,
               int64_t e) {
-  const int64_t foot = ((heads - 1) * s_head + d) * e;
-  return Extent{span(p, (N - 1) * s_tok * e + foot), s_tok * e, foot};
+  return Extent{span(p, ((N - 1) * s_tok + (heads - 1) * s_head + d) * e), d * e,
+                {s_tok * e, s_head * e}, {N, heads}};
 }
 
-// Whether two of them share a byte.  Rows that lie beside each other in every token, as
-// the parts of one projection do, do not.
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }    // b > 0
+
+// Whether rows at 0, sa, .. (na of them) and at off, off + sb, .. (nb) share a byte.
+bool rows_share(int64_t off, int64_t sa, int64_t na, int64_t sb, int64_t nb, int64_t row) {
+  if (na == 1) sa = sb;
+  if (nb == 1) sb = sa;
+  if (na == 1 && nb == 1) return off < row && off > -row;
+  // rows i and j share one where off + j sb - i sa lies within a row's size
+  auto meets = [&](int64_t at, int64_t s, int64_t lo, int64_t hi) {      // at - m s, lo <= m <= hi
+    const int64_t m = floor_div(at, s);
+    return (m >= lo && m <= hi && at - m * s < row) ||
+           (m + 1 >= lo && m + 1 <= hi && (m + 1) * s - at < row);
+  };
+  if (sa == sb) return meets(off, sa, 1 - nb, na - 1);
+  if (nb > 65535) return true;                     // not looked at one by one
+  for (int64_t j = 0; j < nb; ++j)
+    if (meets(off + j * sb, sa, 0, na - 1)) return true;
+  return false;
+}
+
+// Whether two of them share a byte.  The parts of one projection's rows do not, be they
+// beside each other in every token or alternating head by head.  Strides that are not told
+// apart here count as shared.
 bool share(const Extent& a, const Extent& b) {
   if (!overlap(a.s, b.s)) return false;
-  if (a.tok != b.tok || a.foot > a.tok || b.foot > b.tok) return true;
-  const uintptr_t t = static_cast<uintptr_t>(a.tok);
-  const uintptr_t off = b.s.lo >= a.s.lo ? (b.s.lo - a.s.lo) % t : (t - (a.s.lo - b.s.lo) % t) % t;
-  return off < static_cast<uintptr_t>(a.foot) || off + static_cast<uintptr_t>(b.foot) > t;
+  const int64_t off = static_cast<int64_t>(b.s.lo) - static_cast<int64_t>(a.s.lo);
+  for (int out = 0; out < 2; ++out) {              // tokens outermost, or heads
+    const int in = 1 - out;
+    const bool am = a.count[out] > 1, bm = b.count[out] > 1;
+    if (am && bm && a.step[out] != b.step[out]) continue;
+    const int64_t t = am ? a.step[out] : b.step[out];
+    auto at = [&](int64_t o) {
+      return rows_share(o, a.step[in], a.count[in], b.step[in], b.count[in], a.row);
+    };
+    if (!am && !bm) return at(off);
+    if (a.foot(out) > t || b.foot(out) > t) continue;
+    // only those of a and b can meet that begin less than t apart
+    const int64_t m = floor_div(off, t), lo = 1 - b.count[out], hi = a.count[out] - 1;
+    return (m >= lo && m <= hi && at(off - m * t)) ||
+           (m + 1 >= lo && m + 1 <= hi && at(off - (m + 1) * t));
+  }
+  return true;
 }
 
 kvc_status check_heads(const kvc_rotary_params* rp, const void* p, int32_t heads, int64_t s_tok,

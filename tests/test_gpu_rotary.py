@@ -132,6 +132,25 @@ def test_in_place_is_the_same(layout, interleaved, norm):
     assert torch.equal(x[:, 8:], before[:, 8:]) and torch.equal(x[..., :pad], before[..., :pad])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("planes", [False, True])
+def test_in_place_where_heads_alternate(planes, dtype):
+    """Queries, keys and values of a head beside each other, in tokens' rows or in planes."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    N, H, d = 45, 5, 64
+    x = torch.randn((H, 3, N, d) if planes else (N, H, 3, d), generator=g, device="cuda").to(DT[dtype])
+    before = x.clone()
+    q, k, v = ((x[:, i].transpose(0, 1) if planes else x[:, :, i]) for i in range(3))
+    q0, k0 = q.clone(), k.clone()
+    pos = torch.randint(0, 5000, (N,), generator=g, device="cuda", dtype=torch.int32)
+    turns = kvc.rotary_turns(d)[0].cuda()
+    kvc.kvc_rotate_heads(kvc.rotary_params(q, k, q, k, d), q, k, pos, turns, q, k)
+    torch.cuda.synchronize()
+    for a, b in ((q, q0), (k, k0)):
+        _check(a, *_reference(b, pos, d, 10000.0, False, False, None), DT[dtype])
+    assert torch.equal(v, before[:, 2].transpose(0, 1) if planes else before[:, :, 2])
+
+
 def test_rows_of_no_token_stay():
     q = torch.randn((8, 3, 128), device="cuda").to(torch.bfloat16)
     q[2] = math.nan

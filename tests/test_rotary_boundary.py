@@ -121,6 +121,66 @@ def test_overlaps():
     assert _call(p, q=at(0), k=at(4), q_out=FAKE + 4 * FAR, k_out=at(7)) == kvc.KVC_ERR_ALIAS
 
 
+def _shared(a, b, row, N):
+    """Whether two of a byte's rows are the same one, by looking at all of them."""
+    (p, heads, s_tok, s_head), (p2, heads2, s_tok2, s_head2) = a, b
+    mine = {p + t * s_tok + h * s_head + i for t in range(N) for h in range(heads) for i in range(row)}
+    return any(p2 + t * s_tok2 + h * s_head2 + i in mine
+               for t in range(N) for h in range(heads2) for i in range(row))
+
+
+@no_gpu
+@pytest.mark.parametrize("N", [1, 2, 5])
+def test_heads_that_alternate(N):
+    """In place where the heads of queries, keys and values take turns in a token's row, or in
+    planes of their own with the tokens inside."""
+    def try_(q, k, q_tok, q_head, k_tok, k_head, heads=4, kv=4, **out):
+        p = _rp(n_tokens=N, n_q_heads=heads, n_kv_heads=kv, q_s_tok=q_tok, q_s_head=q_head, k_s_tok=k_tok,
+                k_s_head=k_head, q_out_s_tok=q_tok, q_out_s_head=q_head, k_out_s_tok=k_tok, k_out_s_head=k_head)
+        a = dict(q=FAKE + 2 * q, k=FAKE + 2 * k, q_out=FAKE + 2 * q, k_out=FAKE + 2 * k)
+        a.update(out)
+        return _call(p, **a)
+    went_on = kvc.KVC_ERR_CUDA                               # to the launch, which finds no GPU
+    assert try_(0, 64, 768, 192, 768, 192) == went_on        # [N, heads, 3, d]
+    assert try_(64, 0, 768, 192, 768, 192) == went_on
+    assert try_(0, 7 * 64, 4 * 576, 576, 4 * 576, 576) == went_on          # [N, H, group + 2, d]
+    assert try_(0, 64, 64, 3 * 64 * N, 64, 3 * 64 * N) == (went_on if N == 1 else kvc.KVC_ERR_ALIAS)
+    assert try_(0, 64 * N, 64, 3 * 64 * N, 64, 3 * 64 * N) == went_on      # [heads, 3, N, d]
+    assert try_(0, 64, 768, 192, 768, 768, kv=1) == went_on  # one key head beside many
+    assert try_(0, 128, 768, 192, 768, 768, kv=1) == went_on
+    # keys in every second gap; at the queries' places; half a row off
+    assert try_(0, 64, 768, 192, 768, 384, kv=2) == went_on
+    assert try_(0, 192, 768, 192, 768, 384, kv=2) == kvc.KVC_ERR_ALIAS
+    assert try_(0, 96, 768, 192, 768, 192, kv=3) == went_on
+    assert try_(0, 32, 768, 192, 768, 192) == kvc.KVC_ERR_ALIAS
+    assert try_(0, 160, 768, 192, 768, 192, kv=3) == kvc.KVC_ERR_ALIAS
+
+
+@no_gpu
+def test_overlaps_of_all_small_layouts():
+    """No call that shares a byte passes, and none without one is refused where the heads'
+    strides are alike or the tokens' rows apart."""
+    import itertools
+    N, row = 3, 4                                            # bytes: 2 elements of bf16
+    refused = passed = 0
+    for q_tok, q_head, k_tok, k_head, off, (hq, hk) in itertools.product(
+            (2, 6, 14), (2, 4, 8), (2, 6, 14), (2, 4, 8), range(-16, 18, 1), ((2, 2), (1, 2), (3, 1))):
+        p = _rp(n_tokens=N, n_q_heads=hq, n_kv_heads=hk, d=2, rot_dim=2, q_s_tok=64, q_s_head=8, k_s_tok=k_tok,
+                k_s_head=k_head, q_out_s_tok=q_tok, q_out_s_head=q_head, k_out_s_tok=64, k_out_s_head=8)
+        st = _call(p, q=FAKE + FAR, k=FAKE + 2 * off, q_out=FAKE, k_out=FAKE + 6 * FAR)
+        a, b = (0, hq, 2 * q_tok, 2 * q_head), (2 * off, hk, 2 * k_tok, 2 * k_head)
+        own = len({x + t * q_tok + h * q_head for t in range(N) for h in range(hq) for x in range(2)}) < 2 * N * hq
+        if own:                                              # rows of the output itself
+            continue
+        if _shared(a, b, row, N):
+            assert st == kvc.KVC_ERR_ALIAS, (a, b)
+            refused += 1
+        elif q_tok == k_tok and ((hq - 1) * q_head < q_tok - 1 and (hk - 1) * k_head < k_tok - 1):
+            assert st == kvc.KVC_ERR_CUDA, (a, b)
+            passed += 1
+    assert refused > 100 and passed > 100
+
+
 def test_binding_refusals():
     q, k = torch.zeros((5, 4, 64)), torch.zeros((5, 2, 64))
     ok = kvc.rotary_params(q, k, q, k, 64)
