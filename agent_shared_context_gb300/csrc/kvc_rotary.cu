@@ -268,6 +268,16 @@ bool rows_share(int64_t off, int64_t sa, int64_t na, int64_t sb, int64_t nb, int
   return false;
 }
 
+// Whether two rows of it share a byte.
+bool folded(const Extent& x) {
+  for (int out = 0; out < 2; ++out)
+    if (x.count[out] == 1 || x.foot(out) <= x.step[out]) return false;
+  // neither nests in the other: the heads' distances beside the tokens'
+  for (int64_t h = 1; h < x.count[1]; ++h)
+    if (rows_share(h * x.step[1], x.step[0], x.count[0], x.step[0], 1, x.row)) return true;
+  return false;
+}
+
 // Whether two of them share a byte.  The parts of one projection's rows do not, be they
 // beside each other in every token or alternating head by head.  Strides that are not told
 // apart here count as shared.
@@ -412,6 +422,8 @@ kvc_status kvc_rotate_heads(const kvc_rotary_params* rp, const void* q, const vo
                         part[i].out_name));
     in[i] = extent(part[i].in, N, part[i].heads, part[i].in_tok, part[i].in_head, d, e);
     out[i] = extent(part[i].out, N, part[i].heads, part[i].out_tok, part[i].out_head, d, e);
+    if (folded(out[i]))
+      return fail(KVC_ERR_ALIAS, "%s: rows overlap one another", part[i].out_name);
     for (const Span& s : fixed)
       if (s.lo != 0 && overlap(out[i].s, s))
         return fail(KVC_ERR_ALIAS, "%s overlaps positions, turns or weights", part[i].out_name);

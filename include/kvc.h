@@ -566,7 +566,8 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
  * will do; where bases and strides are multiples of 16 bytes (and rot_dim of 32
  * bytes, unless interleaved) the rows are read as whole vectors.  Outputs may be
  * the inputs themselves (the same address and strides), and may not overlap
- * anything else that is read; q and k may be parts of one projection's rows.
+ * anything else that is read, nor one another's rows or their own; q and k may be
+ * parts of one projection's rows, one behind the other or head by head.
  * ------------------------------------------------------------------------- */
 typedef struct kvc_rotary_params {
   int32_t n_tokens;     /* N, 0 .. 2^30                                      */

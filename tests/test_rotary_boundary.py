@@ -181,6 +181,31 @@ def test_overlaps_of_all_small_layouts():
     assert refused > 100 and passed > 100
 
 
+@no_gpu
+def test_outputs_whose_rows_overlap():
+    """Two rows of an output at the same bytes would be written by two CTAs."""
+    N, heads, d = 3, 3, 4
+    seen = set()
+    for s_tok in range(d, 30):
+        for s_head in range(d, 30):
+            rows = sorted(t * s_tok + h * s_head for t in range(N) for h in range(heads))
+            want = kvc.KVC_ERR_CUDA if all(b - a >= d for a, b in zip(rows, rows[1:])) else kvc.KVC_ERR_ALIAS
+            for x in "qk":
+                p = _rp(n_tokens=N, n_q_heads=heads, n_kv_heads=heads, d=d, rot_dim=d, q_s_tok=12, q_s_head=4,
+                        k_s_tok=12, k_s_head=4, q_out_s_tok=12, q_out_s_head=4, k_out_s_tok=12, k_out_s_head=4)
+                setattr(p, x + "_out_s_tok", s_tok)
+                setattr(p, x + "_out_s_head", s_head)
+                assert _call(p) == want, (s_tok, s_head)
+            seen.add(want)
+    assert len(seen) == 2
+    # one token or one head: nothing to fold; the inputs may
+    assert _call(_rp(n_tokens=1, q_out_s_tok=64)) == _call(_rp(n_q_heads=1, q_out_s_head=0)) == kvc.KVC_ERR_CUDA
+    assert _call(_rp(q_s_tok=64)) == kvc.KVC_ERR_CUDA
+    assert _call(_rp(q_out_s_tok=64)) == kvc.KVC_ERR_ALIAS
+    # tokens within heads
+    assert _call(_rp(q_out_s_head=640, q_out_s_tok=64)) == kvc.KVC_ERR_CUDA
+
+
 def test_binding_refusals():
     q, k = torch.zeros((5, 4, 64)), torch.zeros((5, 2, 64))
     ok = kvc.rotary_params(q, k, q, k, 64)
