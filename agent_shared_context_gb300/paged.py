@@ -181,6 +181,20 @@ class PagedCache:
         if rows is None:
             self._loaded = K.shape[3]
 
+    def _load_merged(self, K: torch.Tensor, V: torch.Tensor, own_K: torch.Tensor,
+                     own_V: torch.Tensor, rows: torch.Tensor) -> None:
+        """``load`` of K and V with ``rows`` out of own_K and own_V, in one write, a layer at a
+        time: written over, the blocks would keep the exponents of the rows replaced and round
+        the others a second time."""
+        self._take(K, V, own_K, own_V, rows)
+        with torch.cuda.stream(self.stream):
+            mine = rows[:, None, None, :, None]
+            for i in range(self.pg.L):
+                k, v = (torch.where(mine, x[:, i:i + 1], y[:, i:i + 1])
+                        for x, y in ((own_K, K), (own_V, V)))
+                self._put(k, v, self.slots, i, False)
+        self._loaded = K.shape[3]
+
     def rotate(self, rotary: Rotary, q: torch.Tensor, k: torch.Tensor,
                w_q: Optional[torch.Tensor] = None, w_k: Optional[torch.Tensor] = None,
                q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
@@ -284,8 +298,12 @@ def from_chain(runner: ChainRunner, agent: int, n_q_heads: int, new_tokens: int,
                     R * max(T, new_tokens), device=K.device, stream=runner.stream,
                     scale_block=scale_block)
     pc.plan([T] * R, R * T)
-    pc.load(K, V)
-    if not runner.own_prefix(agent):
+    if runner.own_prefix(agent):
+        pc.load(K, V)
+    elif pc.scaled:
+        pc._load_merged(K, V, runner.inp.exact_K[agent], runner.inp.exact_V[agent], ~runner.ph_rows)
+    else:
+        pc.load(K, V)
         pc.load(runner.inp.exact_K[agent], runner.inp.exact_V[agent], ~runner.ph_rows)
     return pc
 

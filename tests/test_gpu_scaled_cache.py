@@ -143,3 +143,32 @@ def test_demonstration(capsys):
     paged.main(["--workload", "llama2k", "--layers", "1", "--prompt", "20", "--steps", "4", "--cache", "e4m3",
                 "--rotary"])
     assert "e4m3" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_pages_of_a_chain_that_reuses_its_buffers(own_stream):
+    """The agent's rows are rounded once: as if its whole cache had been written, with nothing
+    left of the agent whose buffer it took over."""
+    from agent_shared_context_gb300.chain import ChainRunner
+    wl = synth.scaled(synth.workload("llama2k"), L=2, H=2, R=3, seg_len=[64, 72], pf=24)
+    inp = synth.generate(wl, device="cuda")
+    agent = wl.n_agents - 1
+    for x in (inp.exact_K[agent - 2], inp.exact_V[agent - 2]):    # whose buffer that is
+        x.mul_(64.0)
+    torch.cuda.synchronize()
+    runner = ChainRunner(wl, inp, keep_outputs=False, stream=torch.cuda.Stream() if own_stream else None)
+    torch.cuda.synchronize()                              # its buffers are made on this stream
+    runner.run()
+    assert not runner.own_prefix(agent)
+    pc = paged.from_chain(runner, agent, 8, 4, 16, "e4m3", 16)
+    torch.cuda.synchronize()
+    mask = runner.ph_rows[:, None, None, :, None]
+    whole = [torch.where(mask, x, y) for x, y in zip(runner.held(agent), (inp.exact_K[agent], inp.exact_V[agent]))]
+    want = paged.PagedCache(wl.L, wl.H, wl.d, "e4m3", 8, pc.pg.n_pages, 16, wl.R, pc.pg.max_blocks,
+                            wl.R * wl.T, scale_block=16)
+    want.plan([wl.T] * wl.R)
+    want.load(*whole)
+    torch.cuda.synchronize()
+    assert torch.equal(pc.table, want.table) and torch.equal(pc.kv_lens, want.kv_lens)
+    for name in ("pool_K", "pool_V", "exp_K", "exp_V"):
+        assert torch.equal(getattr(pc, name), getattr(want, name)), name
