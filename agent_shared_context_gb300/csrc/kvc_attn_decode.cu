@@ -479,6 +479,11 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t stream) {
 // requests of 1,000 keys 11.9 us (23.6), 16 of 4,000 54 (59), 32 of 1,000 38 (44), 64 of
 // 4,000 181 (179); all tokens one request's, 10,240 keys: 8 of them 40 us (48), 16 65
 // (50), 32 114 (52), 64 214 (61).
+// Scaled pools go by the same rule, whose border is not theirs: the chunk kernel converts
+// whole tiles for the few rows.  There 32 requests of 4,000 keys take 59 us, and 64, of 256
+// rows, 310 where the decoding kernel would take 109; 128 of them 600 (211); 64 of 10,240
+// 673 (260); heads of 64, 64 of 4,000 253 (78); all tokens one request's, 10,240 keys: 8
+// of them 30 us, 16 41, 32 69, 64 73 (122).
 bool attn_decode_fits(const AttnArgs& a) {
   return a.N <= a.R && a.G <= 16 && static_cast<int64_t>(a.N) * a.G <= 128;
 }

@@ -15,10 +15,11 @@
 //   l   = sum_j 2^(x_j - m),            m = max x_j,
 //   O   = sum_j 2^(x_j + b_j - r) v8_j, r = max (x_j + b_j) - 14,
 //   out = O 2^(r - m) / l.
-// 2^(x_j + b_j - r) lies below 2^14 and its largest above 2^13, whatever the blocks'
-// exponents are; as fp16 it is off by 2^-12 of itself, or by 2^-39 of the row's largest,
-// which is little beside the output's rounding to bf16 (2^-9).  q 2^-u has its largest
-// element in [2^14, 2^15): all of bf16's bits remain but for elements 2^28 times smaller.
+// The largest 2^(x_j + b_j - r) is 2^14, whatever the blocks' exponents are; as fp16 each
+// is off by 2^-11 of itself, or by 2^-39 of the row's largest.  The first is little beside
+// the output's rounding to bf16 (2^-8), and the second wherever the largest term has a part
+// in the output's element.  q 2^-u has its largest element in [2^14, 2^15): all of bf16's
+// bits remain but for elements 2^28 times smaller.
 //
 // An 8 x 16-byte matrix comes out of shared memory by ldmatrix as if its elements had 16
 // bits: a lane gets four neighbouring columns of a key, so K's columns enter the MMA in
@@ -28,9 +29,12 @@
 //
 // Measured, 32 query heads on 8 of 128: 16 requests of 10,240 keys, blocks of 16, 69.7 us,
 // 341 MB at 4.9 TB/s (bf16 pools 109 us, twice the bytes); one request of 131,072 keys 62
-// us (87); one of 777 keys 9.0 us.  Of this some 10 us are beginning and end; the rest is
-// bound by the instructions of a step (some 900 for 32 keys) on two warps in each quarter
-// of the SM: three CTAs of fewer registers (spills) 73 us, two stages instead of three 71.
+// us (87); one of 777 keys 9.0 us; heads of 64: 51, 46 and 8.6 us.  Of this some 10 us are
+// beginning and end; the rest is bound by the latency of a step (some 900 instructions for
+// 32 keys, from ldmatrix through conversion, product, maximum and exponentials to the
+// second product), which two warps in each quarter of the SM do not hide: 37% of the
+// cycles issue one.  Three CTAs of fewer registers (spills) 73 us, two stages instead of
+// three 71.
 //
 // Keys that no row sees are filled with zeros.  A tile of which only some rows see a part
 // is looked through for NaNs in V (there are no infinities); with one in it the product

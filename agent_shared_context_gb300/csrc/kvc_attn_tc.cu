@@ -84,7 +84,7 @@
 // A pair of row tiles takes some 6,000 cycles for 128 keys, a half 3,000: 420 to its
 // first scores, 560 for their largest, 1,120 for P, the rest rescales and waits.  512
 // threads leave it 128 registers and a fourth warp in each quarter of the SM: 3,300
-// instructions per quarter and tile pair (bf16 1,750), 53% of the cycles issue one.
+// instructions per quarter and tile pair (bf16 1,750), 52% of the cycles issue one.
 // Tried: two converting warps of 168 registers 689 us; one warp that copies and looks up
 // for all four 590 to 633; bulk copies for runs of rows 445, as fast but with more
 // roles; 64 scores at once in registers (spills) 565; registers moved between warpgroups

@@ -18,8 +18,12 @@
 // written as whole 32-byte sectors.  Measured: two trajectories of 10,240 tokens, 32
 // layers, 8 heads of 128, blocks of 32, 582 us, 6.9 TB/s (with a maximum, a slot and an
 // address worked out for each row by itself 1,074 us: three of four cycles issued an
-// instruction).  A step's 16 tokens take 14.8 us and 2,048 tokens 18, most of it the
-// host's; the kernels 6.7 and 8.8 with cold caches.
+// instruction).  That is for rows in step with their blocks, 16 of which lie in one block;
+// others are still worked out row by row.  With 16 layers: blocks of 16 in step 288 us, 7.0
+// TB/s; from rows 5 and 42 on 511 us, 3.9; of 10,250 tokens, one trajectory of two in step, 393 us.
+// One layer, in a replayed graph: a step's 16 tokens 6.1 us, 2,048 tokens 11.2 (a chain of
+// slots, leaders, maxima, exponents and stores, with barriers between); by itself a call
+// is the host's 15 to 18.
 #include <cuda_bf16.h>
 
 #include "kvc_attn_sched.cuh"
@@ -182,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) page_write_scaled_kernel(const __gri
   }
   __syncthreads();
 
-  // Where a warp's rows are all of one block, as they are in a long source, they have one
-  // maximum, one exponent and no place of their own to look up but the pool's.
+  // Where a warp's rows are all of one block, as in a long source whose 16 rows begin where
+  // blocks (of a multiple of 16 rows) do, they have one maximum, one exponent and no place of their own to look up but the pool's.
   const int mine = leader[warp * kWarpRows + (lane & (kWarpRows - 1))];
   const int lead0 = __shfl_sync(0xffffffffu, mine, 0);
   const bool together = __all_sync(0xffffffffu, mine == lead0 && mine >= 0);

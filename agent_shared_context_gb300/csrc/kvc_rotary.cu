@@ -6,7 +6,8 @@
 // angle, and 64-bit arithmetic is slow here.  But only the angle's part of a turn
 // matters, and that is an integer product: with F_i = f_i / (2 pi) in units of 2^-64
 // turns, p F_i mod 2^64 is the angle as a fraction of a turn, exact but for F's own
-// 2^-53.  Its upper 32 bits go through sincospi.
+// error, a few 2^-53 of p F_i.  Its upper 32 bits, as fp32 off by 2^-26 of a turn, go
+// through sincospi.
 //
 // One CTA has a token: its pairs' cosines and sines are made once, in shared memory,
 // while the heads' values are on their way, and serve all heads.  A row (one head) lies

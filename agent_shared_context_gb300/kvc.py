@@ -570,9 +570,9 @@ def rotary_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", fac
     """(turns, amplitude): the pairs' frequencies base^(-2 i / rot_dim) as turns per
     position in units of 2^-64, a host int64 tensor [rot_dim / 2] (``.cuda()`` it once),
     and the rotation's amplitude.  ``scaling`` for long contexts: "none", "linear" (all
-    divided by ``factor``), "bands" (those that make at least ``high`` turns within
+    divided by ``factor``), "bands" (model configurations say "llama3": those that make at least ``high`` turns within
     ``original`` positions stay, those of at most ``low`` are divided, the share kept
-    between is linear in the turns) or "ramp" (it is linear in the pair's number, and the
+    between is linear in the turns) or "ramp" ("yarn": it is linear in the pair's number, and the
     amplitude grows with the factor)."""
     import torch
     if scaling not in _MODES:

@@ -11,8 +11,9 @@ PH rows, its own PF rows; KVCMAS listing, Figure 1(c)) becomes the context
 that its new tokens attend to.
 
 With dtype "e4m3" the pools hold bytes, numbers of 8 bits with a power of two for each
-block of tokens and head (half of bf16's memory and of decoding's time); rows go in and
-queries attend as bf16.  ``rotate`` turns a step's queries and keys by the positions that
+block of tokens and head: half of bf16's memory; decoding with up to 128 rows of queries a
+KV head takes 0.64 to 0.71 of bf16's time, with more of them 1.7 times (64 requests of
+4,000 tokens, 32 heads on 8), prompts 1.25 to 1.4 times.  Rows go in and queries attend as bf16.  ``rotate`` turns a step's queries and keys by the positions that
 ``plan`` gave them, with the heads' norms where the model has some.
 
 Nothing here waits for the device: lengths, tables and the stack of free pages

@@ -559,8 +559,9 @@ kvc_status kvc_paged_attention(const kvc_paged* pg, const kvc_attn_params* at, c
  *   i < rot_dim / 2, the pairs being (y[i], y[i + rot_dim / 2]), with interleaved
  *   == 1 (y[2 i], y[2 i + 1]):
  *     (a, b) -> amplitude (a cos - b sin, b cos + a sin);
- *   the others stay.  The arithmetic is fp32, rounded once; the angle is exact to
- *   2^-31 of a turn at any position.
+ *   the others stay.  The arithmetic is fp32, rounded once; the angle is off by 2^-26
+ *   of a turn, at any position, and by a few 2^-53 of itself, the table's own error
+ *   (some 2^-25 of a turn where positions reach 2^31).
  * `turns` [rot_dim / 2] is DEVICE memory: f_i in turns per position, in units of
  * 2^-64, as kvc_rotary_turns gives them.  Any strides (elements) with d contiguous
  * will do; where bases and strides are multiples of 16 bytes (and rot_dim of 32
@@ -592,13 +593,15 @@ kvc_status kvc_rotate_heads(const kvc_rotary_params* rp, const void* q, const vo
 typedef enum kvc_rotary_mode {
   KVC_ROTARY_PLAIN = 0,
   KVC_ROTARY_LINEAR = 1, /* every frequency / factor                                    */
-  KVC_ROTARY_BANDS = 2,  /* by the turns made within `original` positions: those of at
-                            least `high` stay, those of at most `low` are divided by
-                            factor, the share kept between them is linear in the turns   */
-  KVC_ROTARY_RAMP = 3    /* by the pair's number: between the (real) numbers of the pairs
-                            that make `high` and `low` turns, rounded outwards and kept
-                            in [0, rot_dim - 1], the share kept falls linearly from 1 to
-                            0; amplitude 0.1 ln(factor) + 1                              */
+  KVC_ROTARY_BANDS = 2,  /* "llama3" in model configurations.  By the turns made within
+                            `original` positions: those of at least `high` stay, those
+                            of at most `low` are divided by factor, the share kept
+                            between them is linear in the turns                          */
+  KVC_ROTARY_RAMP = 3    /* "yarn" in model configurations.  By the pair's number:
+                            between the (real) numbers of the pairs that make `high` and
+                            `low` turns, rounded outwards and kept in [0, rot_dim - 1],
+                            the share kept falls linearly from 1 to 0; amplitude
+                            0.1 ln(factor) + 1                                           */
 } kvc_rotary_mode;
 
 typedef struct kvc_rotary_scaling {
@@ -670,8 +673,8 @@ kvc_status kvc_page_write_scaled(const kvc_paged* pg, const kvc_scales* sc, int3
  * Chunks bring the numbers of 32 neighbouring keys (from a multiple of 32 on) to one
  * exponent, exactly where K's differ by up to 15 and V's by up to 10, and take those that
  * differ by more key by key; beside others, K's blocks of exponent -100 (of zeros, or of
- * elements below 2^-91) may count as zeros.  Keys whose weight is below 2^-90 of the row's largest may
- * be left out.  A NaN in sight gives NaN.
+ * elements below 2^-91) may count as zeros.  Keys whose weight is below 2^-90 of the
+ * row's largest may be left out.  A NaN in sight gives NaN.
  * The workspace follows the same rules, with its own size.
  * ------------------------------------------------------------------------- */
 size_t kvc_paged_attention_scaled_workspace(const kvc_paged* pg, const kvc_attn_params* at,
