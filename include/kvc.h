@@ -674,7 +674,8 @@ kvc_status kvc_page_write_scaled(const kvc_paged* pg, const kvc_scales* sc, int3
  * exponent, exactly where K's differ by up to 15 and V's by up to 10, and take those that
  * differ by more key by key; beside others, K's blocks of exponent -100 (of zeros, or of
  * elements below 2^-91) may count as zeros.  Keys whose weight is below 2^-90 of the
- * row's largest may be left out.  A NaN in sight gives NaN.
+ * row's largest may be left out.  Chunks' sums carry V's exponents too: their lse is off
+ * by a few 2^-24 times the largest of these besides.  A NaN in sight gives NaN.
  * The workspace follows the same rules, with its own size.
  * ------------------------------------------------------------------------- */
 size_t kvc_paged_attention_scaled_workspace(const kvc_paged* pg, const kvc_attn_params* at,
